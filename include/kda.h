@@ -299,10 +299,127 @@ kda_status_t kda_bwd(const void* q, const void* k, const void* v, const void* g,
                      const int32_t* cu_seqlens, int32_t batch, int64_t seqlen, int32_t num_heads,
                      int32_t head_dim_k, int32_t head_dim_v, int32_t num_seqs, kda_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Softmax attention beside the KDA layers.  Models that use KDA interleave it with ordinary
+ * (grouped-query) softmax-attention layers; these entry points run those layers' serving step next
+ * to kda_decode, and the gradient of their norm + rotation for training:
+ *     kda_qk_norm_rope (+ _bwd)   per-head RMS norm of queries and keys, then the position rotation
+ *     kda_kv_append               the same, with keys and values written into a paged cache
+ *     kda_kv_read                 cached rows read back
+ *     kda_attn_decode             attention of one or a few new tokens over the cache
+ *
+ * Layouts.  Token tensors are bf16, head sizes multiples of 16 up to 128 (KDA_ERR_UNSUPPORTED
+ * otherwise).  The inputs q, k, v of the first three are rows [tokens][heads][D] whose tokens lie
+ * q_stride, k_stride, v_stride elements apart (multiples of 8, at least heads * D), so they may be
+ * parts of one projection's output; outputs are contiguous.
+ *   The paged cache: k_cache, v_cache [num_pages][num_kv_heads][page_size][D], pages k_page_stride /
+ * v_page_stride elements apart (16 bytes' multiple, at least num_kv_heads * page_size * D, below
+ * 2^38), page_size a power of two from 8 to 1024, num_pages * page_size < 2^31.  Either bf16 (k_scale
+ * and v_scale NULL), or e4m3 codes with fp32 scales k_scale, v_scale [num_pages][num_kv_heads]
+ * [page_size] (contiguous), one per row: a row's values are code * scale.
+ *   Slot s is row s % page_size of page s / page_size.  A sequence's tokens 0, 1, .. lie in the pages
+ * of its page_table row [max_pages] in order; entries beyond its last page are not read.
+ *   16-byte aligned: every bf16 tensor, the caches, weights and the rotation table; the others 4-byte.
+ *
+ * Device-side checks.  Positions, slots, page numbers and lengths live on the device.  What is out of
+ * range there is never read or written through; it is recorded as KDA_ERR_INVALID_ARGUMENT in the
+ * workspace's status word (kda_read_device_status), and
+ *   - a token whose position or slot is out of range is skipped: its output rows stay as they were;
+ *   - a length below 0 counts as 0, one beyond the table (max_pages * page_size) as that;
+ *   - kda_kv_read leaves the rows of a page number out of range, and kda_attn_decode reads page 0 in
+ *     its place (that sequence's results are then meaningless).
+ * The workspace of the first three and kda_kv_read is optional as in kda_decode (256 bytes, aligned to
+ * 256, the status word first; zero it once). */
+
+/* q_out = rotation(norm(q)), k_out = rotation(norm(k)), per token and head, in fp32, rounded once:
+ *     n_c = x_c / sqrt(mean(x^2) + eps) * weight_c         (weight NULL: n = x; eps is then not used)
+ *     y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin    for the pairs (a, b) of the first rot_dim
+ * channels: (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved = 1; the others pass.
+ *   q_weight, k_weight  fp32 [D] or NULL (each on its own)
+ *   cos_sin     fp32 [max_positions][rot_dim]: the cosines of a position's rot_dim / 2 angles, then
+ *               the sines; rot_dim a multiple of 16 up to D, 0 for no rotation (table and positions unused)
+ *   positions   int32 [tokens]
+ * Either of q and k may be left out (num_q_heads or num_kv_heads 0).  In place (q_out = q, k_out = k)
+ * where the input is contiguous. */
+kda_status_t kda_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+                              const float* q_weight, const float* k_weight, float eps, const float* cos_sin,
+                              const int32_t* positions, void* q_out, void* k_out, int64_t tokens,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim,
+                              int32_t max_positions, int32_t interleaved, void* workspace, kda_stream_t stream);
+
+/* Bytes of workspace kda_qk_norm_rope_bwd needs: a 256-byte header (status word first) and the
+ * blocks' partial sums of the weights' gradients. */
+size_t kda_qk_norm_rope_bwd_workspace_size(void);
+
+/* The gradients of sum(d_q_out * q_out) + sum(d_k_out * k_out): dq, dk bf16 (contiguous), and
+ * dq_weight, dk_weight fp32 [D] (overwritten; given exactly where the weight is).  d_q_out and d_k_out
+ * are contiguous; dq may be d_q_out and dk d_k_out.  The sums over tokens run in a fixed order: the
+ * same call gives the same bits. */
+kda_status_t kda_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, const void* q, const void* k,
+                                  int64_t q_stride, int64_t k_stride, const float* q_weight,
+                                  const float* k_weight, float eps, const float* cos_sin,
+                                  const int32_t* positions, void* dq, void* dk, float* dq_weight,
+                                  float* dk_weight, int64_t tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, int32_t rot_dim, int32_t max_positions, int32_t interleaved,
+                                  void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* kda_qk_norm_rope with the keys, and the values as they are, written to the cache: token t's rows to
+ * slots[t] (int32).  A negative slot skips its token (padding: nothing of it is read or written, q_out
+ * included); the non-negative slots of a call must be distinct.  q may be left out (num_q_heads 0).
+ * An e4m3 row gets scale = max(max_c |x_c| / 448, 2^-64) and codes round(x / scale) of its fp32
+ * values; a row that holds an infinity or NaN gets the scale NaN and codes 0, so it reads as NaN. */
+kda_status_t kda_kv_append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const float* q_weight, const float* k_weight, float eps,
+                           const float* cos_sin, const int32_t* positions, void* q_out, void* k_cache,
+                           void* v_cache, float* k_scale, float* v_scale, const int32_t* slots, int64_t tokens,
+                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim,
+                           int32_t max_positions, int32_t interleaved, int32_t num_pages, int32_t page_size,
+                           int64_t k_page_stride, int64_t v_page_stride, void* workspace, kda_stream_t stream);
+
+/* Rows cu_seqlens[n] .. cu_seqlens[n + 1] of k_out and v_out (bf16 [total_tokens][num_kv_heads][D])
+ * receive tokens 0, 1, .. of sequence n, as bf16(code * scale) from an e4m3 cache.  cu_seqlens int32
+ * [num_seqs + 1] = 0 = cu[0] <= cu[1] <= .. <= cu[num_seqs] <= total_tokens, no sequence longer than
+ * max_pages * page_size; otherwise nothing is written and the status word records it.  Rows behind the
+ * last sequence stay as they were.  page_table int32 [num_seqs][max_pages]. */
+kda_status_t kda_kv_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                         const int32_t* page_table, const int32_t* cu_seqlens, void* k_out, void* v_out,
+                         int32_t num_seqs, int64_t total_tokens, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t num_pages, int32_t page_size, int32_t max_pages, int64_t k_page_stride,
+                         int64_t v_page_stride, void* workspace, kda_stream_t stream);
+
+/* Bytes of workspace kda_attn_decode needs: a 256-byte header (status word first), and the partial
+ * results of the pieces that the cache's length is split into.  Independent of batch and lengths; no
+ * part of it has to be initialised (but the status word, if it is to be read). */
+size_t kda_attn_decode_workspace_size(int32_t new_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
+
+/* Attention of each sequence's last new_tokens tokens over its cached keys and values, theirs
+ * included (append first).  Query t of sequence b stands at position p = seq_lens[b] - new_tokens + t;
+ * head h reads kv head h / (num_q_heads / num_kv_heads), and sees the keys j <= p, with window > 0 only
+ * j > p - window:
+ *     z_j = scale * q . k_j,  with softcap > 0: z_j <- softcap * tanh(z_j / softcap)
+ *     out = sum_j exp(z_j) v_j / sum_j exp(z_j),   lse = log sum_j exp(z_j)
+ * A query that sees no key (a length of 0, or fewer tokens than new_tokens) gets out = 0 and lse = -inf.
+ * Whatever the rows a query does not see hold, NaN included, does not reach it, except for e4m3 codes
+ * that are NaN themselves in rows that some other query of the sequence sees (kda_kv_append writes none).
+ *   q, out      bf16 [batch][new_tokens][num_q_heads][D] (out not in q's place);  lse fp32
+ *               [batch][new_tokens][num_q_heads] or NULL
+ *   page_table  int32 [batch][max_pages] (max_pages * page_size <= 2^30), seq_lens int32 [batch].
+ *               Sequences may share pages.  With a window, entries of pages before it are not read.
+ *   workspace   kda_attn_decode_workspace_size bytes, 256-byte aligned; calls that share one must be
+ *               ordered (the same stream, or events).
+ * One pass over the cache in two launches (one, where no sequence can be longer than a piece); fp32
+ * scores, softmax statistics and sums.  The order of all sums is fixed by the sizes and lengths. */
+kda_status_t kda_attn_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, const int32_t* page_table, const int32_t* seq_lens, float scale,
+                             float softcap, int32_t window, void* out, float* lse, int32_t batch, int32_t new_tokens,
+                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
+                             int32_t page_size, int32_t max_pages, int64_t k_page_stride, int64_t v_page_stride,
+                             void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
 /* Synchronises `stream`, reads the workspace's sticky status word, clears it, and returns
  * KDA_OK or the recorded device error: KDA_ERR_DEVICE_TIMEOUT (a bounded wait ran out; reported
- * first when both are recorded) or KDA_ERR_INVALID_ARGUMENT (cu_seqlens out of order, or a decode
- * state index past the pool).
+ * first when both are recorded) or KDA_ERR_INVALID_ARGUMENT (cu_seqlens out of order, a decode state
+ * index past the pool, or a position, slot, page or length of the attention operators out of range).
  * KDA_ERR_CUDA if the copy fails. */
 kda_status_t kda_read_device_status(void* workspace, kda_stream_t stream);
 

@@ -12,6 +12,9 @@ PyTorch supplies device memory and the current stream.
     decode(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound,
            state_in, state_out, state_indices)             # batched recurrent step on a state pool
 
+and, for the softmax-attention layers beside the KDA ones (attention.py): qk_norm_rope,
+qk_norm_rope_bwd, kv_append, kv_read and attn_decode.
+
 The argument order of ``fwd`` follows FlashKDA's ``fwd`` as printed in the vLLM PR #54859 report
 (test_flashkda_near_collinear_keys_remain_finite); ``chunk_kda`` follows the fla call on the page
 "What CUDA Version Is Required to Use FlashKDA?", section Usage Examples.
@@ -24,11 +27,16 @@ from typing import Optional, Tuple
 
 import torch
 
+from . import attention
+from .attention import (attn_decode, attn_decode_workspace_size, kv_append, kv_read, new_attn_decode_workspace,
+                        qk_norm_rope, qk_norm_rope_bwd)
+
 __all__ = ["get_workspace_size_ex", "fwd", "fwd_recurrent", "decode", "segment_map", "state_affine", "bwd", "bwd_workspace_size",
            "checkpoint_size", "fwd_checkpointed", "FLAG_GATE_PRECOMPUTED", "FLAG_NO_QK_L2NORM",
            "FLAG_BETA_PRECOMPUTED", "get_workspace_size", "fwd_launch_count", "new_workspace",
            "is_supported", "chunk_kda", "read_device_status", "selftest_wait_timeout", "KDAError",
-           "library_path", "load"]
+           "library_path", "load", "qk_norm_rope", "qk_norm_rope_bwd", "kv_append", "kv_read", "attn_decode",
+           "attn_decode_workspace_size", "new_attn_decode_workspace"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "lib", "libkda_b200.so")
@@ -103,6 +111,7 @@ def load():
     lib.kda_read_device_status.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
+    attention._declare(lib)
     _lib = lib
     return lib
 

@@ -1,0 +1,984 @@
+// Attention of one or a few new tokens per sequence over the paged key-value cache.
+//
+// Row r = (new token t, query head) of a sequence and its kv head h sees the keys j of the cache with
+// j <= p (p = len - new + t, its own position) and, with a window W, j > p - W:
+//     z_j = scale q . K_j,  capped: z = cap tanh(z / cap);   o = sum_j e^{z_j} V_j / sum_j e^{z_j}
+// in one pass over K and V with the running maximum m and sum l of the softmax (base 2).
+//
+// What bounds it: every key and value row is read once and used by G T rows (G query heads per kv
+// head, T new tokens), 4 G T flops per 2 x 2 bytes (bf16): HBM, until G T is near 64.  So the design
+// is a stream of cache tiles with little else:
+//   - Split: the (sequence, kv head, row block) units are laid end to end as blocks of 4 tiles of
+//     keys, and every CTA (two per SM) takes an equal share of all blocks, wherever it begins and
+//     ends, so ragged lengths cost no balance.  A unit that several CTAs share leaves fp32 partial
+//     results (o, m, l) in the workspace, joined in a fixed order by a second, dependent launch.
+//   - Each of a CTA's 4 warps streams its own tiles (one per block) through its own ring of stages,
+//     with no CTA barrier inside a unit: TMA loads of the K and V rows through 4-D maps (channel,
+//     token in page, head, page), swizzled for conflict-free matrix loads; an e4m3 cache's scales
+//     follow by 4-byte cp.async on the same barrier.  ~190 KB of copies in flight per SM.
+//   - Up to 16 rows (32 where a unit has more) form one mma.sync m16n8k16 operand; these instructions
+//     run far below their rate here (a tile's 48 take ~100 of the ~360 cycles its bytes take).
+//   - bf16 cache: P enters the second product as a bf16 pair hi + lo, so its rounding (2^-17) stays
+//     below that of the bf16 output.  e4m3 cache: codes are exact in fp16; the key's scale multiplies
+//     the score, and the value's enters the exponent, w_j = 2^(z_j + log2 s_j - M) with M the running
+//     maximum of that sum, so w is in (0, 1] whatever the scales are; times 2^14 it is rounded to fp16
+//     (2^-11 down to 2^-28 of the maximum).  q (bf16) is scaled by a power of two per row to fit fp16.
+#include <cuda_fp16.h>
+
+#include "attn_common.cuh"
+#include "kda_device.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = 2 * 160;  // bound used for the workspace (148 SMs on a B200)
+constexpr float kWeightShift = 14.0f;
+
+struct DecodeMaps {
+  CUtensorMap k, v;
+};
+
+struct DecodeParams {
+  AttnDecodeArgs a;
+  int32_t group, rows, row_blocks;  // rows = new_tokens * group, of one (sequence, kv head)
+  float* part_o;                    // [2 * CTAs][rows per block][d]
+  float2* part_ml;                  // [2 * CTAs][rows per block]
+  int4* meta;                       // [CTAs]: first partial, partials, unit, 0
+  uint32_t* status;
+};
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          sm100::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on `bar` once this thread's earlier cp.async copies are done.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (kHalf)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  __half2 t = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&t);
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Tile geometry.  kDP: the head size padded to 64 or 128 channels (the padding is zero in q and in
+// the loaded rows); kTok: keys of one warp's tile, 8 KB of K and V together (4 KB for 64 e4m3
+// channels); a block is one tile per warp.
+template <bool kFp8, int kDP>
+struct Geo {
+  static constexpr int kTok = kFp8 ? 32 : (kDP == 128 ? 16 : 32);
+  static constexpr int kRowBytes = kFp8 ? kDP : 128;               // bytes of a row in one column block
+  static constexpr int kColBlocks = kFp8 ? 1 : kDP / 64;           // 128-byte column blocks (bf16)
+  static constexpr int kOpBytes = kTok * kRowBytes * kColBlocks;   // K (or V) of one tile
+  static constexpr int kStageBytes = 2 * kOpBytes;
+  static constexpr int kStages = 24576 / kStageBytes;              // 3 (6 for 4 KB tiles)
+  static constexpr int kBlockTok = kTok * kWarps;
+  static constexpr int kScaleBytes = kFp8 ? 2 * kTok * 4 : 0;
+};
+
+// Byte offset of 16-byte chunk `chunk` of row `row` in a swizzled block of kRowBytes-wide rows.
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t chunk) {
+  return kRowBytes == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+}
+
+// Keys [lo, hi) that any row of a sequence sees.
+__device__ __forceinline__ void key_range(const AttnDecodeArgs& a, int b, int& lo, int& hi, uint32_t* status) {
+  int len = a.seq_lens[b];
+  const int64_t cap = (int64_t)a.max_pages << a.page_shift;
+  if (len < 0 || len > cap) {
+    if (status) atomicOr(status, kStatusBadIndex);
+    len = len < 0 ? 0 : (int)cap;
+  }
+  hi = len;
+  const int64_t first = a.window > 0 ? (int64_t)len - a.new_tokens - a.window + 1 : 0;
+  lo = first > 0 ? (int)first : 0;
+}
+
+// Blocks of one unit of the sequence; an empty one counts one block (its output still has to be written).
+template <int kBlockTok>
+__device__ __forceinline__ int num_blocks(int lo, int hi) {
+  const int n = (hi + kBlockTok - 1) / kBlockTok - lo / kBlockTok;
+  return n > 0 ? n : 1;
+}
+
+template <bool kFp8, int kDP, int kMT>
+struct Smem {
+  using G = Geo<kFp8, kDP>;
+  static constexpr int kRows = 16 * kMT;
+  static constexpr int kQFragBytes = kMT > 1 ? kMT * (kDP / 16) * 32 * 16 : 0;
+  static constexpr int kStageOff = 0;
+  static constexpr int kWarpBytes = G::kStages * G::kStageBytes;
+  static constexpr int kScaleOff = kWarps * kWarpBytes;
+  static constexpr int kQOff = kScaleOff + kWarps * G::kStages * G::kScaleBytes;
+  static constexpr int kMlOff = kQOff + kQFragBytes;                     // [2][warps][rows] floats
+  static constexpr int kBarOff = kMlOff + 2 * kWarps * kRows * 4;
+  static constexpr int kScanOff = kBarOff + kWarps * G::kStages * 8;     // 8 int64
+  static constexpr int kTotal = kScanOff + 128;
+  static constexpr int kPitch = kDP + 4;                                 // floats, of the merge buffers
+  static_assert(kRows * kPitch * 4 <= kWarpBytes, "merge buffer fits a warp's stages");
+};
+
+template <bool kFp8, int kDP, int kMT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const __grid_constant__ DecodeMaps maps,
+                                                                           const __grid_constant__ DecodeParams p) {
+  using G = Geo<kFp8, kDP>;
+  using SM = Smem<kFp8, kDP, kMT>;
+  constexpr int kTok = G::kTok, kNT = kTok / 8, kKS = kDP / 16, kDT = kDP / 8, kRows = SM::kRows;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (sm100::smem_u32(smem_raw) & 1023)) & 1023);
+  const AttnDecodeArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  uint8_t* stages = smem + SM::kStageOff + warp * SM::kWarpBytes;
+  float* scales = reinterpret_cast<float*>(smem + SM::kScaleOff) + warp * G::kStages * (G::kScaleBytes / 4);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBarOff) + warp * G::kStages;
+  float* s_m = reinterpret_cast<float*>(smem + SM::kMlOff);
+  float* s_l = s_m + kWarps * kRows;
+  int64_t* s_scan = reinterpret_cast<int64_t*>(smem + SM::kScanOff);
+  __shared__ int s_abort;
+  __shared__ int s_b;
+  __shared__ int64_t s_off;
+
+  sm100::griddep_launch_dependents();
+  if (tid == 0) s_abort = 0;
+  if (lane == 0) {
+    for (int i = 0; i < G::kStages; ++i) sm100::mbar_init(&bars[i], kFp8 ? 33 : 1);
+    sm100::fence_mbar_init();
+  }
+
+  // ---- this CTA's share [w0, w1) of all blocks, and the sequence it begins in
+  const int64_t units_per_seq = (int64_t)a.hkv * p.row_blocks;
+  const int per = (a.batch + kThreads - 1) / kThreads;
+  const int b_first = tid * per, b_last = min(a.batch, b_first + per);
+  int64_t mine = 0;
+  for (int b = b_first; b < b_last; ++b) {
+    int lo, hi;
+    key_range(a, b, lo, hi, blockIdx.x == 0 ? p.status : nullptr);
+    mine += num_blocks<G::kBlockTok>(lo, hi) * units_per_seq;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  const int64_t ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
+  const int64_t cta = blockIdx.x;
+  if (cta >= ctas) {
+    if (tid == 0) p.meta[cta] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  const int64_t w0 = cta * total / ctas, w1 = (cta + 1) * total / ctas;
+  if (mine > 0 && before <= w0 && w0 < before + mine) {
+    int64_t at = before;
+    for (int b = b_first; b < b_last; ++b) {
+      int lo, hi;
+      key_range(a, b, lo, hi, nullptr);
+      const int64_t n = num_blocks<G::kBlockTok>(lo, hi) * units_per_seq;
+      if (w0 < at + n) {
+        s_b = b;
+        s_off = w0 - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  int b = s_b;
+  int64_t off = s_off;
+
+  const int page_mask = (1 << a.page_shift) - 1;
+  const int box_rows = min(kTok, page_mask + 1);
+  const float base_scale = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
+  int stage_in = 0, stage_out = 0;
+  uint32_t phase_out = 0;
+  int4 meta = make_int4(0, 0, 0, 0);
+
+  for (int64_t w = w0; w < w1;) {
+    // ---- one unit's blocks [blk, blk + take) of this CTA
+    int lo, len;
+    key_range(a, b, lo, len, nullptr);
+    const int n_blk = num_blocks<G::kBlockTok>(lo, len);
+    const int u = (int)(off / n_blk), blk = (int)(off - (int64_t)u * n_blk);
+    const int take = (int)min((int64_t)(n_blk - blk), w1 - w);
+    const int h = u / p.row_blocks, rb = u - h * p.row_blocks;
+    const int row_base = rb * kRows;
+    const int tok0 = (lo / G::kBlockTok + blk) * G::kBlockTok + warp * kTok;  // this warp's first tile
+    // tiles that hold a key in [lo, len)
+    int i_begin = 0, i_end = take;
+    while (i_end > 0 && tok0 + (i_end - 1) * G::kBlockTok >= len) --i_end;
+    while (i_begin < i_end && tok0 + i_begin * G::kBlockTok + kTok <= lo) ++i_begin;
+
+    // page of the key that this lane stands for in tile i (of the nearest key in [lo, len))
+    auto page_of = [&](int i) {
+      int tok = tok0 + i * G::kBlockTok + (lane & (kTok - 1));
+      tok = tok < lo ? lo : (tok >= len ? len - 1 : tok);
+      return a.page_table[(int64_t)b * a.max_pages + (tok >> a.page_shift)];
+    };
+    auto issue = [&](int i, int page) {
+      if ((uint32_t)page >= (uint32_t)a.num_pages) {  // never read outside the cache
+        if (p.status) atomicOr(p.status, kStatusBadIndex);
+        page = 0;
+      }
+      const int t0 = tok0 + i * G::kBlockTok;
+      uint8_t* st = stages + stage_in * G::kStageBytes;
+      uint64_t* bar = &bars[stage_in];
+      if (lane == 0) sm100::mbar_arrive_expect_tx(bar, G::kStageBytes);
+      for (int r = 0; r < kTok; r += box_rows) {
+        const int pg = __shfl_sync(0xffffffffu, page, r);
+        if (lane == 0) {
+          const int at = (t0 + r) & page_mask;
+#pragma unroll
+          for (int cb = 0; cb < G::kColBlocks; ++cb) {
+            uint8_t* dst = st + cb * (kTok * G::kRowBytes) + r * G::kRowBytes;
+            tma_load_4d(dst, &maps.k, bar, cb * 64, at, h, pg);
+            tma_load_4d(dst + G::kOpBytes, &maps.v, bar, cb * 64, at, h, pg);
+          }
+        }
+      }
+      if (kFp8) {
+        const int64_t s = (((int64_t)page * a.hkv + h) << a.page_shift) + ((t0 + lane) & page_mask);
+        const uint32_t dst = sm100::smem_u32(scales + stage_in * 2 * kTok + lane);
+        cp_async4(dst, a.k_scale + s);
+        cp_async4(dst + kTok * 4, a.v_scale + s);
+        cp_async_arrive(bar);
+      }
+      if (++stage_in == G::kStages) stage_in = 0;
+    };
+
+    int page_next = i_begin < i_end ? page_of(i_begin) : 0;
+    int i_issue = i_begin;
+    for (int k = 0; k < G::kStages - 1 && i_issue < i_end; ++k) {
+      const int page = page_next;
+      if (i_issue + 1 < i_end) page_next = page_of(i_issue + 1);
+      issue(i_issue++, page);
+    }
+
+    // ---- the rows' queries as fragments, their key ranges
+    uint32_t qf[kMT == 1 ? kKS : 1][4];
+    float rscale[kMT][2];   // score factor of rows g and g + 8
+    int row_hi[kMT][2], row_lo[kMT][2];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+      const __nv_bfloat16* src[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int r = row_base + mt * 16 + s * 8 + g;
+        const bool ok = r < p.rows;
+        const int t = ok ? r / p.group : 0;
+        const int head = h * p.group + (ok ? r - t * p.group : 0);
+        src[s] = ok ? a.q + (((int64_t)b * a.new_tokens + t) * a.hq + head) * a.d : nullptr;
+        const int pos = len - a.new_tokens + t;
+        row_hi[mt][s] = ok ? pos + 1 : 0;
+        row_lo[mt][s] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+        rscale[mt][s] = base_scale;
+      }
+      uint32_t f[kKS][4];
+      if (!kFp8) {
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int ch = ks * 16 + (j >> 1) * 8 + 2 * c;
+            f[ks][j] = src[j & 1] && ch < a.d ? __ldg(reinterpret_cast<const unsigned int*>(src[j & 1] + ch)) : 0u;
+          }
+      } else {
+        // channels 64 j + 16 c + 4 s + {0..3} are k-step 4 j + s of this thread (as the key bytes are read)
+        float x[2][kDP / 64][16];
+        float big[2] = {0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int j = 0; j < kDP / 64; ++j) {
+            const int ch = 64 * j + 16 * c;
+            uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (src[s] && ch < a.d) {
+              v[0] = __ldg(reinterpret_cast<const uint4*>(src[s] + ch));
+              v[1] = __ldg(reinterpret_cast<const uint4*>(src[s] + ch) + 1);
+            }
+            const uint32_t wv[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 t = unpack_bf16(wv[i]);
+              x[s][j][2 * i] = t.x;
+              x[s][j][2 * i + 1] = t.y;
+              big[s] = fmaxf(big[s], fmaxf(fabsf(t.x), fabsf(t.y)));
+            }
+          }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          big[s] = fmaxf(big[s], __shfl_xor_sync(0xffffffffu, big[s], 1));
+          big[s] = fmaxf(big[s], __shfl_xor_sync(0xffffffffu, big[s], 2));
+          // the power of two below the row's largest magnitude (exact factors)
+          int e = (int)((__float_as_uint(big[s]) >> 23) & 255) - 127;
+          e = big[s] == 0.f || e > 126 ? 0 : (e < -100 ? -100 : e);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          rscale[mt][s] *= __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+          for (int j = 0; j < kDP / 64; ++j)
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              f[4 * j + q4][s] = pack_half(x[s][j][4 * q4] * down, x[s][j][4 * q4 + 1] * down);
+              f[4 * j + q4][s + 2] = pack_half(x[s][j][4 * q4 + 2] * down, x[s][j][4 * q4 + 3] * down);
+            }
+        }
+      }
+      if (kMT == 1) {
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) qf[kMT == 1 ? ks : 0][j] = f[ks][j];
+      } else if (warp == 0) {  // (the other warps formed the same)
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks)
+          reinterpret_cast<uint4*>(smem + SM::kQOff)[(mt * kKS + ks) * 32 + lane] = make_uint4(f[ks][0], f[ks][1], f[ks][2], f[ks][3]);
+      }
+    }
+    if (kMT > 1) __syncthreads();
+
+    float o[kMT][kDT][4];
+    float m[kMT][2], l[kMT][2];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+#pragma unroll
+      for (int j = 0; j < kDT; ++j) o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.f;
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+    // tiles whose every key every row sees need no mask
+    const int all_hi = len - a.new_tokens + 1, all_lo = a.window > 0 ? len - a.window : 0;
+
+    int done = i_begin;  // tiles consumed
+    for (int i = i_begin; i < i_end; ++i) {
+      if (i_issue < i_end) {
+        const int page = page_next;
+        if (i_issue + 1 < i_end) page_next = page_of(i_issue + 1);
+        issue(i_issue++, page);
+      }
+      const bool arrived = bounded_wait(&bars[stage_out], phase_out, &s_abort, p.status);
+      if (!__all_sync(0xffffffffu, arrived)) break;
+      uint8_t* st = stages + stage_out * G::kStageBytes;
+      const uint32_t ks_addr = sm100::smem_u32(st), vs_addr = ks_addr + G::kOpBytes;
+      const float* sc = scales + stage_out * 2 * kTok;
+      const int t0 = tok0 + i * G::kBlockTok;
+      const bool edge = t0 + kTok > all_hi || t0 < all_lo;
+
+      // ---- S = Q K^T
+      float s[kMT][kNT][4];
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+      if (!kFp8) {
+        const uint32_t mrow = ((lane >> 4) << 3) + (lane & 7), mchunk = (lane >> 3) & 1;
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks) {
+          uint32_t qa[kMT][4];
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt) {
+            if (kMT == 1) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) qa[mt][j] = qf[kMT == 1 ? ks : 0][j];
+            } else {
+              const uint4 t = reinterpret_cast<const uint4*>(smem + SM::kQOff)[(mt * kKS + ks) * 32 + lane];
+              qa[mt][0] = t.x; qa[mt][1] = t.y; qa[mt][2] = t.z; qa[mt][3] = t.w;
+            }
+          }
+#pragma unroll
+          for (int n2 = 0; n2 < kNT / 2; ++n2) {
+            uint32_t kb[4];
+            ldsm4(kb, ks_addr + (ks >> 2) * (kTok * 128) + swz<128>(n2 * 16 + mrow, (ks & 3) * 2 + mchunk));
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) {
+              mma16816<false>(s[mt][2 * n2], qa[mt], kb[0], kb[1]);
+              mma16816<false>(s[mt][2 * n2 + 1], qa[mt], kb[2], kb[3]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kDP / 64; ++j) {
+          uint32_t qa[kMT][4][4];
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              if (kMT == 1) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) qa[mt][q4][x] = qf[kMT == 1 ? 4 * j + q4 : 0][x];
+              } else {
+                const uint4 t = reinterpret_cast<const uint4*>(smem + SM::kQOff)[(mt * kKS + 4 * j + q4) * 32 + lane];
+                qa[mt][q4][0] = t.x; qa[mt][q4][1] = t.y; qa[mt][q4][2] = t.z; qa[mt][q4][3] = t.w;
+              }
+            }
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            const uint4 kb = *reinterpret_cast<const uint4*>(st + swz<G::kRowBytes>(nt * 8 + g, 4 * j + c));
+            const uint32_t wv[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              const uint32_t b0 = e4m3x2_to_half2(wv[q4]), b1 = e4m3x2_to_half2(wv[q4] >> 16);
+#pragma unroll
+              for (int mt = 0; mt < kMT; ++mt) mma16816<true>(s[mt][nt], qa[mt][q4], b0, b1);
+            }
+          }
+        }
+      }
+
+      // ---- scores in base 2, masks, the value scales' logarithms
+      float inv_vs[kFp8 ? kNT : 1][2];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        float kf[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+        if (kFp8) {
+          const float2 k2 = *reinterpret_cast<const float2*>(sc + nt * 8 + 2 * c);
+          const float2 v2 = *reinterpret_cast<const float2*>(sc + kTok + nt * 8 + 2 * c);
+          kf[0] = k2.x;
+          kf[1] = k2.y;
+          // (a scale that is not a number makes its row of the cache so: kept)
+          const float vx = v2.x < 0x1p-100f ? 0x1p-100f : v2.x, vy = v2.y < 0x1p-100f ? 0x1p-100f : v2.y;
+          lv[0] = lg2_approx(vx);
+          lv[1] = lg2_approx(vy);
+          inv_vs[kFp8 ? nt : 0][0] = rcp_approx(vx);
+          inv_vs[kFp8 ? nt : 0][1] = rcp_approx(vy);
+        }
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float z = s[mt][nt][e] * (kFp8 ? kf[e & 1] * rscale[mt][e >> 1] : rscale[mt][e >> 1]);
+            if (a.softcap > 0.f)  // z = cap tanh(z / cap) log2 e
+              z = a.softcap * kLog2e * (1.f - 2.f * rcp_approx(ex2_approx(z * (2.f * kLog2e)) + 1.f));
+            if (kFp8) z += lv[e & 1];
+            if (edge) {
+              const int j = t0 + nt * 8 + 2 * c + (e & 1);
+              if (j >= row_hi[mt][e >> 1] || j < row_lo[mt][e >> 1]) z = -INFINITY;
+            }
+            s[mt][nt][e] = z;
+          }
+      }
+      // ---- running maximum and sum; P in place of S
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt) {
+        float alpha[2];
+        bool moved = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) mx = fmaxf(mx, fmaxf(s[mt][nt][2 * x], s[mt][nt][2 * x + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[mt][x], mx);
+          const float ref = mn == -INFINITY ? 0.f : mn;
+          alpha[x] = ex2_approx(m[mt][x] - ref);
+          moved |= mn > m[mt][x];
+          m[mt][x] = mn;
+          const float shift = kFp8 ? ref - kWeightShift : ref;
+          float sum = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float z = s[mt][nt][2 * x + e];
+              const float pr = ex2_approx(z - shift);
+              s[mt][nt][2 * x + e] = pr;
+              if (!kFp8) sum += pr;
+              else if (!(z == -INFINITY)) sum = fmaf(pr, inv_vs[kFp8 ? nt : 0][e], sum);
+            }
+          l[mt][x] = l[mt][x] * alpha[x] + sum;
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int j = 0; j < kDT; ++j) {
+            o[mt][j][0] *= alpha[0];
+            o[mt][j][1] *= alpha[0];
+            o[mt][j][2] *= alpha[1];
+            o[mt][j][3] *= alpha[1];
+          }
+        }
+      }
+
+      if (edge) {
+        // Rows of V that no query of the unit sees may hold anything (they may never have been
+        // written): zero them, since 0 * inf is not 0.
+        bool wrote = false;
+        for (int r = 0; r < kTok; ++r) {
+          const int j = t0 + r;
+          if (j >= lo && j < len) continue;
+          wrote = true;
+          constexpr int kChunks = G::kColBlocks * G::kRowBytes / 16;
+          if (lane < kChunks)
+            *reinterpret_cast<uint4*>(st + G::kOpBytes + (lane / (G::kRowBytes / 16)) * (kTok * G::kRowBytes) +
+                                      swz<G::kRowBytes>(r, lane % (G::kRowBytes / 16))) = make_uint4(0, 0, 0, 0);
+        }
+        if (!kFp8) {
+          // Keys that some rows see and others do not: an infinity or NaN in such a row of V must
+          // not reach the rows that do not see it.  Take that row out of the product and add it to
+          // the rows that see it, element by element.
+          for (int r = 0; r < kTok; ++r) {
+            const int j = t0 + r;
+            if (j < lo || j >= len || (j < all_hi && j >= all_lo)) continue;
+            constexpr int kChunks = G::kColBlocks * 8;
+            uint4* at = reinterpret_cast<uint4*>(st + G::kOpBytes + (lane / 8) * (kTok * 128) + swz<128>(r, lane % 8));
+            bool odd = false;
+            if (lane < kChunks) {
+              const uint4 v = *at;
+              const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x) odd |= (wv[x] & 0x7f80u) == 0x7f80u || (wv[x] & 0x7f800000u) == 0x7f800000u;
+            }
+            if (!__any_sync(0xffffffffu, odd)) continue;
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                uint32_t bits = 0;  // P[row][r], held by thread (r % 8) / 2 of the row's four (masks: no local array)
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) {
+                  const uint32_t here = nt == r / 8 ? 0xffffffffu : 0u, second = (r & 1) ? 0xffffffffu : 0u;
+                  bits |= here & ((second & __float_as_uint(s[mt][nt][2 * x + 1])) | (~second & __float_as_uint(s[mt][nt][2 * x])));
+                }
+                const float pr = __uint_as_float(__shfl_sync(0xffffffffu, bits, (lane & ~3) | ((r & 7) >> 1)));
+                if (j < row_hi[mt][x] && j >= row_lo[mt][x]) {
+#pragma unroll
+                  for (int dt = 0; dt < kDT; ++dt) {
+                    const float2 v = unpack_bf16(*reinterpret_cast<const uint32_t*>(
+                        st + G::kOpBytes + (dt / 8) * (kTok * 128) + swz<128>(r, dt % 8) + 4 * c));
+                    o[mt][dt][2 * x] = fmaf(pr, v.x, o[mt][dt][2 * x]);
+                    o[mt][dt][2 * x + 1] = fmaf(pr, v.y, o[mt][dt][2 * x + 1]);
+                  }
+                }
+              }
+            __syncwarp();
+            if (lane < kChunks) *at = make_uint4(0, 0, 0, 0);
+            wrote = true;
+          }
+        }
+        if (wrote) sm100::fence_proxy_async();  // before the next TMA load into this stage
+        __syncwarp();
+      }
+
+      // ---- O += P V
+      if (!kFp8) {
+        const uint32_t vrow = lane & 15, vchunk = lane >> 4;
+#pragma unroll
+        for (int kt = 0; kt < kTok / 16; ++kt) {
+          uint32_t hi[kMT][4], lo2[kMT][4];
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              split2(s[mt][2 * kt + (x >> 1)][2 * (x & 1)], s[mt][2 * kt + (x >> 1)][2 * (x & 1) + 1], hi[mt][x], lo2[mt][x]);
+#pragma unroll
+          for (int d2 = 0; d2 < kDT / 2; ++d2) {
+            uint32_t vb[4];
+            ldsm4t(vb, vs_addr + (d2 >> 2) * (kTok * 128) + swz<128>(kt * 16 + vrow, (d2 & 3) * 2 + vchunk));
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) {
+              mma16816<false>(o[mt][2 * d2], hi[mt], vb[0], vb[1]);
+              mma16816<false>(o[mt][2 * d2 + 1], hi[mt], vb[2], vb[3]);
+              mma16816<false>(o[mt][2 * d2], lo2[mt], vb[0], vb[1]);
+              mma16816<false>(o[mt][2 * d2 + 1], lo2[mt], vb[2], vb[3]);
+            }
+          }
+        }
+      } else {
+        // column g of product tile j stands for channel (kDP / 8) g + j: a thread's bytes of a row are contiguous
+        const uint8_t* vst = st + G::kOpBytes;
+#pragma unroll
+        for (int kt = 0; kt < kTok / 16; ++kt) {
+          uint32_t pa[kMT][4];
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              pa[mt][x] = pack_half(s[mt][2 * kt + (x >> 1)][2 * (x & 1)], s[mt][2 * kt + (x >> 1)][2 * (x & 1) + 1]);
+          constexpr int kWords = kDP / 32;  // 32-bit words of a row per thread: 4 or 2
+          uint32_t vw[4][kWords];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = kt * 16 + (x >> 1) * 8 + 2 * c + (x & 1);
+            if (kDP == 128) {
+              const uint4 t = *reinterpret_cast<const uint4*>(vst + swz<G::kRowBytes>(r, g));
+              vw[x][0] = t.x; vw[x][1] = t.y; vw[x][kWords - 2] = t.z; vw[x][kWords - 1] = t.w;
+            } else {
+              const uint2 t = *reinterpret_cast<const uint2*>(vst + swz<G::kRowBytes>(r, g >> 1) + 8 * (g & 1));
+              vw[x][0] = t.x; vw[x][1] = t.y;
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < kWords; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t e0 = __byte_perm(vw[0][x], vw[1][x], y ? 0x7362 : 0x5140);
+              const uint32_t e1 = __byte_perm(vw[2][x], vw[3][x], y ? 0x7362 : 0x5140);
+              const uint32_t b00 = e4m3x2_to_half2(e0), b10 = e4m3x2_to_half2(e1);
+              const uint32_t b01 = e4m3x2_to_half2(e0 >> 16), b11 = e4m3x2_to_half2(e1 >> 16);
+#pragma unroll
+              for (int mt = 0; mt < kMT; ++mt) {
+                mma16816<true>(o[mt][4 * x + 2 * y], pa[mt], b00, b10);
+                mma16816<true>(o[mt][4 * x + 2 * y + 1], pa[mt], b01, b11);
+              }
+            }
+        }
+      }
+      __syncwarp();  // the stage has been read
+      done = i + 1;
+      if (++stage_out == G::kStages) {
+        stage_out = 0;
+        phase_out ^= 1;
+      }
+    }
+
+    // ---- the warps' results together
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 1);
+        l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 2);
+        if (c == 0) {
+          s_m[warp * kRows + mt * 16 + x * 8 + g] = m[mt][x];
+          s_l[warp * kRows + mt * 16 + x * 8 + g] = l[mt][x];
+        }
+      }
+    __syncthreads();
+    if (s_abort) {  // a wait ran out: let this warp's copies land (bounded), then leave
+      for (; done < i_issue; ++done) {
+        sm100::mbar_wait(&bars[stage_out], phase_out, kWaitLimitNs);
+        if (++stage_out == G::kStages) {
+          stage_out = 0;
+          phase_out ^= 1;
+        }
+      }
+      if (tid == 0) p.meta[cta] = make_int4(0, 0, 0, 0);
+      return;
+    }
+    float* buf = reinterpret_cast<float*>(stages);
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = mt * 16 + x * 8 + g;
+        float top = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_m[v * kRows + r]);
+        const float f = m[mt][x] == -INFINITY ? (l[mt][x] == 0.f ? 0.f : 1.f) : ex2_approx(m[mt][x] - top);
+        if (!kFp8) {
+#pragma unroll
+          for (int j = 0; j < kDT; ++j)
+            *reinterpret_cast<float2*>(buf + r * SM::kPitch + 8 * j + 2 * c) = make_float2(o[mt][j][2 * x] * f, o[mt][j][2 * x + 1] * f);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < kDT; j += 4)
+              *reinterpret_cast<float4*>(buf + r * SM::kPitch + kDT * (2 * c + y) + j) =
+                  make_float4(o[mt][j][2 * x + y] * f, o[mt][j + 1][2 * x + y] * f, o[mt][j + 2][2 * x + y] * f, o[mt][j + 3][2 * x + y] * f);
+        }
+      }
+    __syncthreads();
+    const bool whole = blk == 0 && take == n_blk;
+    const bool head_part = w == w0;
+    const int64_t slot = 2 * cta + (head_part ? 0 : 1);
+    const int live = min(kRows, p.rows - row_base);
+    const int d4 = a.d / 4;
+    for (int x = tid; x < live * d4; x += kThreads) {
+      const int r = x / d4, ch = (x - r * d4) * 4;
+      float top = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_m[v * kRows + r]);
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float mv = s_m[v * kRows + r], lv = s_l[v * kRows + r];
+        sum += mv == -INFINITY ? lv : lv * ex2_approx(mv - top);
+        const float4 t = *reinterpret_cast<const float4*>(smem + SM::kStageOff + v * SM::kWarpBytes + (r * SM::kPitch + ch) * 4);
+        acc.x += t.x; acc.y += t.y; acc.z += t.z; acc.w += t.w;
+      }
+      const int row = row_base + r;
+      if (whole) {
+        const int t = row / p.group, head = h * p.group + row - t * p.group;
+        const int64_t at = ((int64_t)b * a.new_tokens + t) * a.hq + head;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2*>(a.out + at * a.d + ch) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        if (ch == 0 && a.lse)
+          a.lse[at] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - (kFp8 ? kWeightShift : 0.f) + log2f(sum)) * 0.6931471805599453f;
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * a.d + ch) = acc;
+        if (ch == 0) p.part_ml[slot * kRows + r] = make_float2(top, sum);
+      }
+    }
+    if (head_part && blk > 0 && blk + take == n_blk) {  // this CTA ends a unit that others began
+      const int64_t start = w - blk;
+      const int64_t c0 = ((start + 1) * ctas - 1) / total;
+      const int64_t first = 2 * c0 + (c0 * total / ctas == start ? 0 : 1);
+      meta = make_int4((int)first, (int)(cta - c0 + 1), (int)((int64_t)b * units_per_seq + u), 0);
+    }
+    w += take;
+    off += take;
+    if (off == n_blk * units_per_seq) {
+      ++b;
+      off = 0;
+    }
+    sm100::fence_proxy_async();  // the merge buffers are stages again
+    __syncthreads();
+  }
+  if (tid == 0) p.meta[cta] = meta;
+}
+
+// Joins the partial results of every unit that more than one CTA worked on, in the order of its
+// keys.  The launch's blocks take (unit, rows) jobs in turn: eight rows, a warp each, where a unit
+// has few partials; one row, its partials dealt to the eight warps, where it has many.
+constexpr int kJoinThreads = 256;
+constexpr int kFewPartials = 8;
+
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ DecodeParams p, int ctas, int rows_per_block,
+                                                                 float weight_shift) {
+  const AttnDecodeArgs& a = p.a;
+  __shared__ int s_end[kMaxCtas];      // jobs up to and with CTA i's unit
+  __shared__ int4 s_meta[kMaxCtas];
+  __shared__ int s_warp[kJoinThreads / 32];
+  __shared__ float s_o[kJoinThreads / 32][kAttnMaxDim];
+  __shared__ float2 s_ml[kJoinThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  sm100::griddep_wait();
+  int jobs[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = 2 * tid + k;
+    if (i < ctas) {
+      const int4 mt = p.meta[i];
+      s_meta[i] = mt;
+      if (mt.y > 0) {
+        const int rb = mt.z % p.row_blocks;
+        const int live = min(rows_per_block, p.rows - rb * rows_per_block);
+        jobs[k] = mt.y > kFewPartials ? live : (live + 7) / 8;
+      }
+    }
+  }
+  int incl = jobs[0] + jobs[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  const int end1 = before + incl, end0 = end1 - jobs[1];
+  if (2 * tid < ctas) s_end[2 * tid] = end0;
+  if (2 * tid + 1 < ctas) s_end[2 * tid + 1] = end1;
+  __syncthreads();
+
+  for (int job = blockIdx.x; job < total; job += gridDim.x) {
+    int lo = 0, hi = ctas - 1;  // the first CTA whose end is beyond the job
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_end[mid] > job) hi = mid;
+      else lo = mid + 1;
+    }
+    const int4 mt = s_meta[lo];
+    const int local = job - (lo > 0 ? s_end[lo - 1] : 0);
+    const int rb = mt.z % p.row_blocks, bh = mt.z / p.row_blocks;
+    const int live = min(rows_per_block, p.rows - rb * rows_per_block);
+    const bool many = mt.y > kFewPartials;
+    const int r = many ? local : local * 8 + warp;
+    const int cta0 = mt.x >> 1;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? mt.x : 2 * (cta0 + i)) * rows_per_block + r; };
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < live) {
+      const int step = many ? kJoinThreads / 32 : 1;
+      for (int i = many ? warp : 0; i < mt.y; i += step) top = fmaxf(top, p.part_ml[slot(i)].x);
+#pragma unroll 4
+      for (int i = many ? warp : 0; i < mt.y; i += step) {
+        const int64_t s = slot(i);
+        const float2 ml = p.part_ml[s];
+        const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - top);
+        sum = fmaf(ml.y, f, sum);
+        if (4 * lane < a.d) {
+          const float4 t = *reinterpret_cast<const float4*>(p.part_o + s * a.d + 4 * lane);
+          acc.x = fmaf(t.x, f, acc.x); acc.y = fmaf(t.y, f, acc.y);
+          acc.z = fmaf(t.z, f, acc.z); acc.w = fmaf(t.w, f, acc.w);
+        }
+      }
+    }
+    if (many) {
+      __syncthreads();
+      reinterpret_cast<float4*>(s_o[warp])[lane] = acc;
+      if (lane == 0) s_ml[warp] = make_float2(top, sum);
+      __syncthreads();
+      if (warp != 0) continue;
+      top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, s_ml[w].x);
+      sum = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kJoinThreads / 32; ++w) {
+        const float f = s_ml[w].x == -INFINITY ? 1.f : ex2_approx(s_ml[w].x - top);
+        sum = fmaf(s_ml[w].y, f, sum);
+        const float4 t = reinterpret_cast<const float4*>(s_o[w])[lane];
+        acc.x = fmaf(t.x, f, acc.x); acc.y = fmaf(t.y, f, acc.y);
+        acc.z = fmaf(t.z, f, acc.z); acc.w = fmaf(t.w, f, acc.w);
+      }
+    }
+    if (r < live) {
+      const int row = rb * rows_per_block + r;
+      const int b = bh / a.hkv, h = bh - b * a.hkv;
+      const int t = row / p.group, head = h * p.group + row - t * p.group;
+      const int64_t at = ((int64_t)b * a.new_tokens + t) * a.hq + head;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      if (4 * lane < a.d)
+        *reinterpret_cast<uint2*>(a.out + at * a.d + 4 * lane) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      if (lane == 0 && a.lse)
+        a.lse[at] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - weight_shift + log2f(sum)) * 0.6931471805599453f;
+    }
+  }
+}
+
+// The cache [pages][heads][page][d] as 4-D (channel, token in page, head, page): boxes of one
+// column block by up to a tile's rows inside one page, zero fill beyond the head size.
+bool make_cache_map(CUtensorMap* map, const void* base, bool fp8, int d, int page, int heads, int pages, int64_t page_stride,
+                    int box_cols, int box_rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t esz = fp8 ? 1 : 2;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)heads, (cuuint64_t)pages};
+  cuuint64_t strides[3] = {d * esz, (cuuint64_t)page * d * esz, (cuuint64_t)page_stride * esz};
+  cuuint32_t box[4] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols * esz == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Rows of one row block: 16 while all rows of a (sequence, kv head) fit, else 32.
+int rows_per_block(int rows) { return rows <= 16 ? 16 : 32; }
+
+template <bool kFp8, int kDP, int kMT>
+cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
+  using G = Geo<kFp8, kDP>;
+  using SM = Smem<kFp8, kDP, kMT>;
+  static bool attr_done[64] = {};
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  DecodeParams p;
+  p.a = a;
+  p.group = a.hq / a.hkv;
+  p.rows = a.new_tokens * p.group;
+  p.row_blocks = (p.rows + SM::kRows - 1) / SM::kRows;
+  const int64_t units = (int64_t)a.batch * a.hkv * p.row_blocks;
+  const int64_t cap = (int64_t)a.max_pages << a.page_shift;
+  const int64_t most_blocks = cap > G::kBlockTok ? (cap + G::kBlockTok - 1) / G::kBlockTok : 1;
+  int64_t grid = (int64_t)kCtasPerSm * sms;
+  if (grid > kMaxCtas) grid = kMaxCtas;
+  if (units < grid && units * most_blocks < grid) grid = units * most_blocks;
+  uint8_t* ws = a.workspace;
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  p.meta = reinterpret_cast<int4*>(ws + kWorkspaceHeader);
+  p.part_ml = reinterpret_cast<float2*>(ws + kWorkspaceHeader + up256(kMaxCtas * sizeof(int4)));
+  p.part_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.part_ml) + up256((size_t)2 * kMaxCtas * SM::kRows * sizeof(float2)));
+  DecodeMaps maps;
+  const int page = 1 << a.page_shift;
+  const int box_rows = page < G::kTok ? page : G::kTok, box_cols = kFp8 ? kDP : 64;
+  if (!make_cache_map(&maps.k, a.k_cache, kFp8, a.d, page, a.hkv, a.num_pages, a.k_page_stride, box_cols, box_rows) ||
+      !make_cache_map(&maps.v, a.v_cache, kFp8, a.d, page, a.hkv, a.num_pages, a.v_page_stride, box_cols, box_rows))
+    return cudaErrorInvalidValue;
+  constexpr uint32_t kSmem = SM::kTotal + 1024;
+  cudaError_t e = set_smem_once(attn_decode_kernel<kFp8, kDP, kMT>, kSmem, attr_done);
+  if (e != cudaSuccess) return e;
+  attn_decode_kernel<kFp8, kDP, kMT><<<(unsigned)grid, kThreads, kSmem, stream>>>(maps, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || most_blocks == 1) return e;  // (no unit has two blocks: nothing to join)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * sms));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel, p, (int)grid, (int)SM::kRows, kFp8 ? kWeightShift : 0.f);
+}
+
+template <bool kFp8, int kDP>
+cudaError_t launch_rows(const AttnDecodeArgs& a, cudaStream_t stream) {
+  return rows_per_block(a.new_tokens * (a.hq / a.hkv)) == 16 ? launch_typed<kFp8, kDP, 1>(a, stream)
+                                                             : launch_typed<kFp8, kDP, 2>(a, stream);
+}
+
+}  // namespace
+
+size_t attn_decode_workspace_bytes(int32_t rows, int32_t d) {
+  const size_t r = rows_per_block(rows);
+  return kWorkspaceHeader + up256(kMaxCtas * sizeof(int4)) + up256(2 * kMaxCtas * r * sizeof(float2)) +
+         up256(2 * kMaxCtas * r * (size_t)d * sizeof(float));
+}
+
+cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream) {
+  if ((int64_t)a.batch * a.new_tokens == 0) return cudaSuccess;
+  if (a.k_scale) return a.d <= 64 ? launch_rows<true, 64>(a, stream) : launch_rows<true, 128>(a, stream);
+  return a.d <= 64 ? launch_rows<false, 64>(a, stream) : launch_rows<false, 128>(a, stream);
+}
+
+}  // namespace kda
