@@ -144,6 +144,10 @@ __device__ __forceinline__ int num_blocks(int lo, int hi) {
   return n > 0 ? n : 1;
 }
 
+// What a unit costs beyond its blocks (queries in, the pipeline filled and drained, the warps' results
+// joined and written), in blocks: the shares of the CTAs are equal in blocks + kUnitCost per unit.
+constexpr int kUnitCost = 3;
+
 template <bool kFp8, int kDP, int kMT>
 struct Smem {
   using G = Geo<kFp8, kDP>;
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   for (int b = b_first; b < b_last; ++b) {
     int lo, hi;
     key_range(a, b, lo, hi, blockIdx.x == 0 ? p.status : nullptr);
-    mine += num_blocks<G::kBlockTok>(lo, hi) * units_per_seq;
+    mine += (num_blocks<G::kBlockTok>(lo, hi) + kUnitCost) * units_per_seq;
   }
   int64_t incl = mine;
 #pragma unroll
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     for (int b = b_first; b < b_last; ++b) {
       int lo, hi;
       key_range(a, b, lo, hi, nullptr);
-      const int64_t n = num_blocks<G::kBlockTok>(lo, hi) * units_per_seq;
+      const int64_t n = (num_blocks<G::kBlockTok>(lo, hi) + kUnitCost) * units_per_seq;
       if (w0 < at + n) {
         s_b = b;
         s_off = w0 - at;
@@ -243,13 +247,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   uint32_t phase_out = 0;
   int4 meta = make_int4(0, 0, 0, 0);
 
+  bool first_part = true;  // no unit has been worked on yet
   for (int64_t w = w0; w < w1;) {
     // ---- one unit's blocks [blk, blk + take) of this CTA
     int lo, len;
     key_range(a, b, lo, len, nullptr);
-    const int n_blk = num_blocks<G::kBlockTok>(lo, len);
-    const int u = (int)(off / n_blk), blk = (int)(off - (int64_t)u * n_blk);
-    const int take = (int)min((int64_t)(n_blk - blk), w1 - w);
+    const int n_blk = num_blocks<G::kBlockTok>(lo, len), n_cost = n_blk + kUnitCost;
+    const int u = (int)(off / n_cost), blk = (int)(off - (int64_t)u * n_cost);
+    const int step = (int)min((int64_t)(n_cost - blk), w1 - w);  // of the unit's cost; its blocks come first
+    const int take = min(n_blk - blk, step);
+    const int64_t w_here = w;
+    w += step;
+    off += step;
+    const int b_here = b;
+    if (off == n_cost * units_per_seq) {
+      ++b;
+      off = 0;
+    }
+    if (take <= 0) continue;
     const int h = u / p.row_blocks, rb = u - h * p.row_blocks;
     const int row_base = rb * kRows;
     const int tok0 = (lo / G::kBlockTok + blk) * G::kBlockTok + warp * kTok;  // this warp's first tile
@@ -262,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     auto page_of = [&](int i) {
       int tok = tok0 + i * G::kBlockTok + (lane & (kTok - 1));
       tok = tok < lo ? lo : (tok >= len ? len - 1 : tok);
-      return a.page_table[(int64_t)b * a.max_pages + (tok >> a.page_shift)];
+      return a.page_table[(int64_t)b_here * a.max_pages + (tok >> a.page_shift)];
     };
     auto issue = [&](int i, int page) {
       if ((uint32_t)page >= (uint32_t)a.num_pages) {  // never read outside the cache
@@ -316,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         const bool ok = r < p.rows;
         const int t = ok ? r / p.group : 0;
         const int head = h * p.group + (ok ? r - t * p.group : 0);
-        src[s] = ok ? a.q + (((int64_t)b * a.new_tokens + t) * a.hq + head) * a.d : nullptr;
+        src[s] = ok ? a.q + (((int64_t)b_here * a.new_tokens + t) * a.hq + head) * a.d : nullptr;
         const int pos = len - a.new_tokens + t;
         row_hi[mt][s] = ok ? pos + 1 : 0;
         row_lo[mt][s] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
@@ -552,22 +567,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         // Rows of V that no query of the unit sees may hold anything (they may never have been
         // written): zero them, since 0 * inf is not 0.
         bool wrote = false;
-        for (int r = 0; r < kTok; ++r) {
-          const int j = t0 + r;
-          if (j >= lo && j < len) continue;
-          wrote = true;
-          constexpr int kChunks = G::kColBlocks * G::kRowBytes / 16;
-          if (lane < kChunks)
-            *reinterpret_cast<uint4*>(st + G::kOpBytes + (lane / (G::kRowBytes / 16)) * (kTok * G::kRowBytes) +
-                                      swz<G::kRowBytes>(r, lane % (G::kRowBytes / 16))) = make_uint4(0, 0, 0, 0);
-        }
+        constexpr int kRowChunks = G::kColBlocks * G::kRowBytes / 16;
+        auto zero_rows = [&](int r0, int r1) {
+          for (int x = r0 * kRowChunks + lane; x < r1 * kRowChunks; x += 32) {
+            const int r = x / kRowChunks, ch = x % kRowChunks;
+            *reinterpret_cast<uint4*>(st + G::kOpBytes + (ch / (G::kRowBytes / 16)) * (kTok * G::kRowBytes) +
+                                      swz<G::kRowBytes>(r, ch % (G::kRowBytes / 16))) = make_uint4(0, 0, 0, 0);
+          }
+          wrote |= r1 > r0;
+        };
+        zero_rows(0, lo - t0);
+        zero_rows(max(len - t0, 0), kTok);
         if (!kFp8) {
           // Keys that some rows see and others do not: an infinity or NaN in such a row of V must
           // not reach the rows that do not see it.  Take that row out of the product and add it to
           // the rows that see it, element by element.
-          for (int r = 0; r < kTok; ++r) {
+          const int low_end = min(max(all_lo - t0, 0), kTok);   // keys [lo, all_lo) and [all_hi, len)
+          for (int r = max(lo - t0, 0); r < min(len - t0, kTok); ++r) {
+            if (r >= low_end && r < all_hi - t0) r = all_hi - t0;
+            if (r >= min(len - t0, kTok)) break;
             const int j = t0 + r;
-            if (j < lo || j >= len || (j < all_hi && j >= all_lo)) continue;
             constexpr int kChunks = G::kColBlocks * 8;
             uint4* at = reinterpret_cast<uint4*>(st + G::kOpBytes + (lane / 8) * (kTok * 128) + swz<128>(r, lane % 8));
             bool odd = false;
@@ -729,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
     __syncthreads();
     const bool whole = blk == 0 && take == n_blk;
-    const bool head_part = w == w0;
+    const bool head_part = first_part;
+    first_part = false;
     const int64_t slot = 2 * cta + (head_part ? 0 : 1);
     const int live = min(kRows, p.rows - row_base);
     const int d4 = a.d / 4;
@@ -750,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       const int row = row_base + r;
       if (whole) {
         const int t = row / p.group, head = h * p.group + row - t * p.group;
-        const int64_t at = ((int64_t)b * a.new_tokens + t) * a.hq + head;
+        const int64_t at = ((int64_t)b_here * a.new_tokens + t) * a.hq + head;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         *reinterpret_cast<uint2*>(a.out + at * a.d + ch) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
         if (ch == 0 && a.lse)
@@ -761,16 +781,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
     }
     if (head_part && blk > 0 && blk + take == n_blk) {  // this CTA ends a unit that others began
-      const int64_t start = w - blk;
+      // the CTA of its first block; the unit is that CTA's first one if its share begins there, or in
+      // the end (without blocks) of the unit before
+      const int64_t start = w_here - blk;
       const int64_t c0 = ((start + 1) * ctas - 1) / total;
-      const int64_t first = 2 * c0 + (c0 * total / ctas == start ? 0 : 1);
-      meta = make_int4((int)first, (int)(cta - c0 + 1), (int)((int64_t)b * units_per_seq + u), 0);
-    }
-    w += take;
-    off += take;
-    if (off == n_blk * units_per_seq) {
-      ++b;
-      off = 0;
+      const int64_t first = 2 * c0 + (start - c0 * total / ctas <= kUnitCost ? 0 : 1);
+      meta = make_int4((int)first, (int)(cta - c0 + 1), (int)((int64_t)b_here * units_per_seq + u), 0);
     }
     sm100::fence_proxy_async();  // the merge buffers are stages again
     __syncthreads();
