@@ -12,10 +12,12 @@
 //     keys, and every CTA (two per SM) takes an equal share of all blocks, wherever it begins and
 //     ends, so ragged lengths cost no balance.  A unit that several CTAs share leaves fp32 partial
 //     results (o, m, l) in the workspace, joined in a fixed order by a second, dependent launch.
-//   - Each of a CTA's 4 warps streams its own tiles (one per block) through its own ring of stages,
-//     with no CTA barrier inside a unit: TMA loads of the K and V rows through 4-D maps (channel,
-//     token in page, head, page), swizzled for conflict-free matrix loads; an e4m3 cache's scales
-//     follow by 4-byte cp.async on the same barrier.  ~190 KB of copies in flight per SM.
+//   - Each of a CTA's 4 warps streams its own tiles (one per block) through its own ring of stages, with
+//     no CTA barrier: 16-byte cp.async copies into swizzled rows (conflict-free matrix loads), kept two
+//     tiles ahead also across the ends of units; about 130 KB of copies in flight per SM.  (TMA boxes
+//     instead cost the issuing warp 800 to 900 cycles a tile, four boxes each, of 2600 to 3400.)
+//   - The warps' results of a unit meet as a chain through shared memory, so that no warp waits for a
+//     slower one before it goes on with the next unit.
 //   - Up to 16 rows (32 where a unit has more) form one mma.sync m16n8k16 operand; these instructions
 //     run far below their rate here (a tile's 48 take ~100 of the ~360 cycles its bytes take).
 //   - bf16 cache: P enters the second product as a bf16 pair hi + lo, so its rounding (2^-17) stays
@@ -34,12 +36,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 2;
-constexpr int kMaxCtas = 2 * 160;  // bound used for the workspace (148 SMs on a B200)
+constexpr int kMaxCtas = kCtasPerSm * 160;  // bound used for the workspace (148 SMs on a B200)
 constexpr float kWeightShift = 14.0f;
-
-struct DecodeMaps {
-  CUtensorMap k, v;
-};
 
 struct DecodeParams {
   AttnDecodeArgs a;
@@ -50,20 +48,17 @@ struct DecodeParams {
   uint32_t* status;
 };
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
-                                            int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-          sm100::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(sm100::smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-// One arrival on `bar` once this thread's earlier cp.async copies are done.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(bar)) : "memory");
+// `bytes` (16 or 0) from src, the rest of the 16 zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -103,19 +98,29 @@ __device__ __forceinline__ float lg2_approx(float x) {
   return y;
 }
 
+// tanh to about 2 units in the last place: below 1 Lambert's continued fraction cut after its fifth
+// denominator, x (945 + 105 x^2 + x^4) / (945 + 420 x^2 + 15 x^4) (off by 6e-8 at 1), above by 1 - 2 / (e^2x + 1).
+__device__ __forceinline__ float tanh_fast(float x) {
+  const float q = x * x;
+  const float near = x * fmaf(q, q + 105.f, 945.f) * rcp_approx(fmaf(q, fmaf(q, 15.f, 420.f), 945.f));
+  const float far = fmaf(-2.f, rcp_approx(ex2_approx(x * (2.f * kLog2e)) + 1.f), 1.f);
+  return q < 1.f ? near : far;
+}
+
 // Tile geometry.  kDP: the head size padded to 64 or 128 channels (the padding is zero in q and in
 // the loaded rows); kTok: keys of one warp's tile, 8 KB of K and V together (4 KB for 64 e4m3
 // channels); a block is one tile per warp.
-template <bool kFp8, int kDP>
+template <bool kFp8, int kDP, int kMT>
 struct Geo {
   static constexpr int kTok = kFp8 ? 32 : (kDP == 128 ? 16 : 32);
   static constexpr int kRowBytes = kFp8 ? kDP : 128;               // bytes of a row in one column block
   static constexpr int kColBlocks = kFp8 ? 1 : kDP / 64;           // 128-byte column blocks (bf16)
   static constexpr int kOpBytes = kTok * kRowBytes * kColBlocks;   // K (or V) of one tile
   static constexpr int kStageBytes = 2 * kOpBytes;
-  static constexpr int kStages = 24576 / kStageBytes;              // 3 (6 for 4 KB tiles)
+  static constexpr int kWarpBytes = kMT == 1 ? 24576 : 16384;
+  static constexpr int kStages = kWarpBytes / kStageBytes;
   static constexpr int kBlockTok = kTok * kWarps;
-  static constexpr int kScaleBytes = kFp8 ? 2 * kTok * 4 : 0;
+  static constexpr int kScaleBytes = kFp8 ? 3 * kTok * 4 : 0;            // k scales; v scales, then their logarithms; reciprocals
 };
 
 // Byte offset of 16-byte chunk `chunk` of row `row` in a swizzled block of kRowBytes-wide rows.
@@ -148,27 +153,60 @@ __device__ __forceinline__ int num_blocks(int lo, int hi) {
 // joined and written), in blocks: the shares of the CTAs are equal in blocks + kUnitCost per unit.
 constexpr int kUnitCost = 3;
 
-template <bool kFp8, int kDP, int kMT>
-struct Smem {
-  using G = Geo<kFp8, kDP>;
-  static constexpr int kRows = 16 * kMT;
-  static constexpr int kQFragBytes = kMT > 1 ? kMT * (kDP / 16) * 32 * 16 : 0;
-  static constexpr int kStageOff = 0;
-  static constexpr int kWarpBytes = G::kStages * G::kStageBytes;
-  static constexpr int kScaleOff = kWarps * kWarpBytes;
-  static constexpr int kQOff = kScaleOff + kWarps * G::kStages * G::kScaleBytes;
-  static constexpr int kMlOff = kQOff + kQFragBytes;                     // [2][warps][rows] floats
-  static constexpr int kBarOff = kMlOff + 2 * kWarps * kRows * 4;
-  static constexpr int kScanOff = kBarOff + kWarps * G::kStages * 8;     // 8 int64
-  static constexpr int kTotal = kScanOff + 128;
-  static constexpr int kPitch = kDP + 4;                                 // floats, of the merge buffers
-  static_assert(kRows * kPitch * 4 <= kWarpBytes, "merge buffer fits a warp's stages");
+// A CTA's share of all units' blocks, piece by piece: next() steps to the blocks [blk, blk + take) of
+// the next unit, until the share is used up.
+template <int kBlockTok>
+struct Walk {
+  int64_t left, off;  // cost left in the share; position of its cursor in sequence next_b
+  int next_b;
+  int b, u, lo, len, n_blk, blk, take;  // the piece
+  __device__ __forceinline__ bool next(const AttnDecodeArgs& a, int64_t units_per_seq) {
+    while (left > 0) {
+      b = next_b;
+      key_range(a, b, lo, len, nullptr);
+      n_blk = num_blocks<kBlockTok>(lo, len);
+      const int n_cost = n_blk + kUnitCost;
+      u = (int)(off / n_cost);
+      blk = (int)(off - (int64_t)u * n_cost);
+      const int step = (int)min((int64_t)(n_cost - blk), left);  // of the unit's cost; its blocks come first
+      take = min(n_blk - blk, step);
+      left -= step;
+      off += step;
+      if (off == n_cost * units_per_seq) {
+        ++next_b;
+        off = 0;
+      }
+      if (take > 0) return true;
+    }
+    return false;
+  }
+  // a warp's tiles of the piece: the first key of tile i is tok0 + i * kBlockTok, i in [i_begin, i_end)
+  // (tiles without a key in [lo, len) are left out)
+  __device__ __forceinline__ void tiles(int warp, int tile_tok, int& tok0, int& i_begin, int& i_end) const {
+    tok0 = (lo / kBlockTok + blk) * kBlockTok + warp * tile_tok;
+    i_end = len > tok0 ? min(take, (len - tok0 - 1) / kBlockTok + 1) : 0;
+    i_begin = min(i_end, tok0 + tile_tok <= lo ? 1 : 0);
+  }
 };
 
 template <bool kFp8, int kDP, int kMT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const __grid_constant__ DecodeMaps maps,
-                                                                           const __grid_constant__ DecodeParams p) {
-  using G = Geo<kFp8, kDP>;
+struct Smem {
+  using G = Geo<kFp8, kDP, kMT>;
+  static constexpr int kRows = 16 * kMT;
+  static constexpr int kQFragBytes = kMT > 1 ? kMT * (kDP / 16) * 32 * 16 : 0;  // one unit's queries
+  static constexpr int kStageOff = 0;
+  static constexpr int kWarpBytes = G::kWarpBytes;
+  static constexpr int kScaleOff = kWarps * kWarpBytes;
+  static constexpr int kQOff = kScaleOff + kWarps * G::kStages * G::kScaleBytes;
+  static constexpr int kSumOff = kQOff + 2 * kQFragBytes;                // the warps' sum: [kRows x kDP] floats,
+  static constexpr int kMlOff = kSumOff + kRows * kDP * 4;               // and each row's maximum and sum
+  static constexpr int kScanOff = kMlOff + kMT * 4 * 32 * 4;             // one int64 per warp
+  static constexpr int kTotal = kScanOff + 8 * kWarps;
+};
+
+template <bool kFp8, int kDP, int kMT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
+  using G = Geo<kFp8, kDP, kMT>;
   using SM = Smem<kFp8, kDP, kMT>;
   constexpr int kTok = G::kTok, kNT = kTok / 8, kKS = kDP / 16, kDT = kDP / 8, kRows = SM::kRows;
   extern __shared__ uint8_t smem_raw[];
@@ -177,20 +215,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   uint8_t* stages = smem + SM::kStageOff + warp * SM::kWarpBytes;
   float* scales = reinterpret_cast<float*>(smem + SM::kScaleOff) + warp * G::kStages * (G::kScaleBytes / 4);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBarOff) + warp * G::kStages;
-  float* s_m = reinterpret_cast<float*>(smem + SM::kMlOff);
-  float* s_l = s_m + kWarps * kRows;
+  float4* s_sum = reinterpret_cast<float4*>(smem + SM::kSumOff) + lane;
+  float4* s_ml = reinterpret_cast<float4*>(smem + SM::kMlOff) + lane;
+  __shared__ int s_any;
   int64_t* s_scan = reinterpret_cast<int64_t*>(smem + SM::kScanOff);
-  __shared__ int s_abort;
   __shared__ int s_b;
   __shared__ int64_t s_off;
 
   sm100::griddep_launch_dependents();
-  if (tid == 0) s_abort = 0;
-  if (lane == 0) {
-    for (int i = 0; i < G::kStages; ++i) sm100::mbar_init(&bars[i], kFp8 ? 33 : 1);
-    sm100::fence_mbar_init();
-  }
 
   // ---- this CTA's share [w0, w1) of all blocks, and the sequence it begins in
   const int64_t units_per_seq = (int64_t)a.hkv * p.row_blocks;
@@ -237,88 +269,106 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     }
   }
   __syncthreads();
-  int b = s_b;
-  int64_t off = s_off;
+  Walk<G::kBlockTok> in, out;  // the pieces whose tiles this warp loads next, and computes next
+  in.left = w1 - w0;
+  in.off = s_off;
+  in.next_b = s_b;
+  out = in;
 
   const int page_mask = (1 << a.page_shift) - 1;
-  const int box_rows = min(kTok, page_mask + 1);
-  const float base_scale = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
+  // scores to base 2 (to the cap's units): a positive factor, its sign goes to the queries, so that
+  // maxima can be taken before it (a factor of zero: zero queries)
+  const float base_scale =
+      a.scale == 0.f ? 1.f : fmaxf(fabsf(a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e), 1.17549435e-38f);
+  const uint32_t q_sign = a.scale < 0.f ? 0x80008000u : 0u;
+
+  // ---- the loading side: a ring of stages, kept full across the units' ends
+  constexpr int kChunks = kDP * (kFp8 ? 1 : 2) / 16, kPass = 32 / kChunks;  // 16-byte chunks of a row; rows a pass
+  const int ld_ch = lane % kChunks, ld_row = lane / kChunks;
+  const int row_bytes = a.d * (kFp8 ? 1 : 2);
+  const uint32_t ld_bytes = 16 * ld_ch < row_bytes ? 16 : 0;   // (channels beyond the head size: zero)
+  const bool one_page = page_mask + 1 >= kTok;                 // a tile lies in one page
+  const uint32_t ring = sm100::smem_u32(stages) + (ld_ch / 8) * (kTok * G::kRowBytes);
+  const int64_t k_step = a.k_page_stride * (kFp8 ? 1 : 2), v_step = a.v_page_stride * (kFp8 ? 1 : 2);
+  const uint8_t* k_base = static_cast<const uint8_t*>(a.k_cache) + (ld_bytes ? 16 * ld_ch : 0);
+  const uint8_t* v_base = static_cast<const uint8_t*>(a.v_cache) + (ld_bytes ? 16 * ld_ch : 0);
   int stage_in = 0, stage_out = 0;
-  uint32_t phase_out = 0;
-  int4 meta = make_int4(0, 0, 0, 0);
-
-  bool first_part = true;  // no unit has been worked on yet
-  for (int64_t w = w0; w < w1;) {
-    // ---- one unit's blocks [blk, blk + take) of this CTA
-    int lo, len;
-    key_range(a, b, lo, len, nullptr);
-    const int n_blk = num_blocks<G::kBlockTok>(lo, len), n_cost = n_blk + kUnitCost;
-    const int u = (int)(off / n_cost), blk = (int)(off - (int64_t)u * n_cost);
-    const int step = (int)min((int64_t)(n_cost - blk), w1 - w);  // of the unit's cost; its blocks come first
-    const int take = min(n_blk - blk, step);
-    const int64_t w_here = w;
-    w += step;
-    off += step;
-    const int b_here = b;
-    if (off == n_cost * units_per_seq) {
-      ++b;
-      off = 0;
+  int in_tok = 0, in_i = 0, in_end = 0, in_h = 0, page_next = 0;
+  bool in_more = true;
+  // to the next tile; this lane's page is that of the key it stands for (of the nearest key in [lo, len))
+  auto advance = [&]() {
+    ++in_i;
+    while (in_i >= in_end) {
+      in_more = in.next(a, units_per_seq);
+      if (!in_more) return;
+      in_h = in.u / p.row_blocks;
+      in.tiles(warp, kTok, in_tok, in_i, in_end);
     }
-    if (take <= 0) continue;
-    const int h = u / p.row_blocks, rb = u - h * p.row_blocks;
-    const int row_base = rb * kRows;
-    const int tok0 = (lo / G::kBlockTok + blk) * G::kBlockTok + warp * kTok;  // this warp's first tile
-    // tiles that hold a key in [lo, len)
-    int i_begin = 0, i_end = take;
-    while (i_end > 0 && tok0 + (i_end - 1) * G::kBlockTok >= len) --i_end;
-    while (i_begin < i_end && tok0 + i_begin * G::kBlockTok + kTok <= lo) ++i_begin;
-
-    // page of the key that this lane stands for in tile i (of the nearest key in [lo, len))
-    auto page_of = [&](int i) {
-      int tok = tok0 + i * G::kBlockTok + (lane & (kTok - 1));
-      tok = tok < lo ? lo : (tok >= len ? len - 1 : tok);
-      return a.page_table[(int64_t)b_here * a.max_pages + (tok >> a.page_shift)];
-    };
-    auto issue = [&](int i, int page) {
+    int tok = in_tok + in_i * G::kBlockTok + (lane & (kTok - 1));
+    tok = tok < in.lo ? in.lo : (tok >= in.len ? in.len - 1 : tok);
+    page_next = a.page_table[(int64_t)in.b * a.max_pages + (tok >> a.page_shift)];
+  };
+  // the copies of the next tile, as one group (empty when there is none left)
+  auto issue = [&]() {
+    if (in_more) {
+      int page = page_next;
       if ((uint32_t)page >= (uint32_t)a.num_pages) {  // never read outside the cache
         if (p.status) atomicOr(p.status, kStatusBadIndex);
         page = 0;
       }
-      const int t0 = tok0 + i * G::kBlockTok;
-      uint8_t* st = stages + stage_in * G::kStageBytes;
-      uint64_t* bar = &bars[stage_in];
-      if (lane == 0) sm100::mbar_arrive_expect_tx(bar, G::kStageBytes);
-      for (int r = 0; r < kTok; r += box_rows) {
-        const int pg = __shfl_sync(0xffffffffu, page, r);
-        if (lane == 0) {
-          const int at = (t0 + r) & page_mask;
+      const int t0 = in_tok + in_i * G::kBlockTok;
+      const uint32_t st = ring + stage_in * G::kStageBytes;
+      auto copy_rows = [&](int i, const uint8_t* ks, const uint8_t* vs) {
+        const uint32_t row = i * kPass + ld_row;
+        const uint32_t dst = st + swz<G::kRowBytes>(row, ld_ch % (G::kRowBytes / 16));
+        cp_async16(dst, ks, ld_bytes);
+        cp_async16(dst + G::kOpBytes, vs, ld_bytes);
+      };
+      if (one_page) {
+        const int64_t line = (((int64_t)in_h << a.page_shift) + (t0 & page_mask) + ld_row) * row_bytes;
+        const uint8_t* ks = k_base + page * k_step + line;
+        const uint8_t* vs = v_base + page * v_step + line;
 #pragma unroll
-          for (int cb = 0; cb < G::kColBlocks; ++cb) {
-            uint8_t* dst = st + cb * (kTok * G::kRowBytes) + r * G::kRowBytes;
-            tma_load_4d(dst, &maps.k, bar, cb * 64, at, h, pg);
-            tma_load_4d(dst + G::kOpBytes, &maps.v, bar, cb * 64, at, h, pg);
-          }
+        for (int i = 0; i < kTok / kPass; ++i) {
+          copy_rows(i, ks, vs);
+          ks += kPass * row_bytes;
+          vs += kPass * row_bytes;
+        }
+      } else {
+#pragma unroll 2
+        for (int i = 0; i < kTok / kPass; ++i) {
+          const int row = i * kPass + ld_row;
+          const int pg = __shfl_sync(0xffffffffu, page, row);
+          const int64_t line = (((int64_t)in_h << a.page_shift) + ((t0 + row) & page_mask)) * row_bytes;
+          copy_rows(i, k_base + pg * k_step + line, v_base + pg * v_step + line);
         }
       }
       if (kFp8) {
-        const int64_t s = (((int64_t)page * a.hkv + h) << a.page_shift) + ((t0 + lane) & page_mask);
-        const uint32_t dst = sm100::smem_u32(scales + stage_in * 2 * kTok + lane);
+        const int64_t s = (((int64_t)page * a.hkv + in_h) << a.page_shift) + ((t0 + lane) & page_mask);
+        const uint32_t dst = sm100::smem_u32(scales + stage_in * 3 * kTok + lane);
         cp_async4(dst, a.k_scale + s);
         cp_async4(dst + kTok * 4, a.v_scale + s);
-        cp_async_arrive(bar);
       }
       if (++stage_in == G::kStages) stage_in = 0;
-    };
-
-    int page_next = i_begin < i_end ? page_of(i_begin) : 0;
-    int i_issue = i_begin;
-    for (int k = 0; k < G::kStages - 1 && i_issue < i_end; ++k) {
-      const int page = page_next;
-      if (i_issue + 1 < i_end) page_next = page_of(i_issue + 1);
-      issue(i_issue++, page);
+      advance();
     }
+    cp_async_commit();
+  };
+  advance();
+#pragma unroll 1
+  for (int k = 0; k < G::kStages - 1; ++k) issue();
 
+  int4 meta = make_int4(0, 0, 0, 0);
+  int pieces = 0;
+  bool more = out.next(a, units_per_seq);
+  while (more) {
+    const int b = out.b, len = out.len, lo = out.lo, blk = out.blk, take = out.take, n_blk = out.n_blk, u = out.u;
+    const int h = u / p.row_blocks, row_base = (u - h * p.row_blocks) * kRows;
+    int tok0, i_begin, i_end;
+    out.tiles(warp, kTok, tok0, i_begin, i_end);
+    more = out.next(a, units_per_seq);
     // ---- the rows' queries as fragments, their key ranges
+    uint4* q_smem = reinterpret_cast<uint4*>(smem + SM::kQOff + (pieces & 1) * SM::kQFragBytes) + lane;
     uint32_t qf[kMT == 1 ? kKS : 1][4];
     float rscale[kMT][2];   // score factor of rows g and g + 8
     int row_hi[kMT][2], row_lo[kMT][2];
@@ -329,9 +379,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       for (int s = 0; s < 2; ++s) {
         const int r = row_base + mt * 16 + s * 8 + g;
         const bool ok = r < p.rows;
+        const bool read = ok && a.scale != 0.f;
         const int t = ok ? r / p.group : 0;
         const int head = h * p.group + (ok ? r - t * p.group : 0);
-        src[s] = ok ? a.q + (((int64_t)b_here * a.new_tokens + t) * a.hq + head) * a.d : nullptr;
+        src[s] = read ? a.q + (((int64_t)b * a.new_tokens + t) * a.hq + head) * a.d : nullptr;
         const int pos = len - a.new_tokens + t;
         row_hi[mt][s] = ok ? pos + 1 : 0;
         row_lo[mt][s] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
@@ -344,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int ch = ks * 16 + (j >> 1) * 8 + 2 * c;
-            f[ks][j] = src[j & 1] && ch < a.d ? __ldg(reinterpret_cast<const unsigned int*>(src[j & 1] + ch)) : 0u;
+            f[ks][j] = src[j & 1] && ch < a.d ? __ldg(reinterpret_cast<const unsigned int*>(src[j & 1] + ch)) ^ q_sign : 0u;
           }
       } else {
         // channels 64 j + 16 c + 4 s + {0..3} are k-step 4 j + s of this thread (as the key bytes are read)
@@ -363,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             const uint32_t wv[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float2 t = unpack_bf16(wv[i]);
+              const float2 t = unpack_bf16(wv[i] ^ q_sign);
               x[s][j][2 * i] = t.x;
               x[s][j][2 * i + 1] = t.y;
               big[s] = fmaxf(big[s], fmaxf(fabsf(t.x), fabsf(t.y)));
@@ -392,13 +443,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
           for (int j = 0; j < 4; ++j) qf[kMT == 1 ? ks : 0][j] = f[ks][j];
-      } else if (warp == 0) {  // (the other warps formed the same)
+      } else {
+        // all four warps write the same; two units' queries alternate, and a warp is at most one unit
+        // ahead of another (the chain of sums below)
 #pragma unroll
-        for (int ks = 0; ks < kKS; ++ks)
-          reinterpret_cast<uint4*>(smem + SM::kQOff)[(mt * kKS + ks) * 32 + lane] = make_uint4(f[ks][0], f[ks][1], f[ks][2], f[ks][3]);
+        for (int ks = 0; ks < kKS; ++ks) q_smem[(mt * kKS + ks) * 32] = make_uint4(f[ks][0], f[ks][1], f[ks][2], f[ks][3]);
       }
     }
-    if (kMT > 1) __syncthreads();
+    if (kMT > 1) __syncwarp();
 
     float o[kMT][kDT][4];
     float m[kMT][2], l[kMT][2];
@@ -412,18 +464,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     // tiles whose every key every row sees need no mask
     const int all_hi = len - a.new_tokens + 1, all_lo = a.window > 0 ? len - a.window : 0;
 
-    int done = i_begin;  // tiles consumed
     for (int i = i_begin; i < i_end; ++i) {
-      if (i_issue < i_end) {
-        const int page = page_next;
-        if (i_issue + 1 < i_end) page_next = page_of(i_issue + 1);
-        issue(i_issue++, page);
-      }
-      const bool arrived = bounded_wait(&bars[stage_out], phase_out, &s_abort, p.status);
-      if (!__all_sync(0xffffffffu, arrived)) break;
+      issue();  // into the stage that the tile before has left
+      cp_async_wait<G::kStages - 1>();
+      __syncwarp();
       uint8_t* st = stages + stage_out * G::kStageBytes;
       const uint32_t ks_addr = sm100::smem_u32(st), vs_addr = ks_addr + G::kOpBytes;
-      const float* sc = scales + stage_out * 2 * kTok;
+      float* sc = scales + stage_out * 3 * kTok;
+      if (kFp8) {
+        // once per key: the logarithm of its value scale and the reciprocal.  (A scale that is not a
+        // number makes the rows that see its key so, by way of the logarithm; its reciprocal stays
+        // finite, for the rows that do not see it.)
+        const float v = sc[kTok + lane];
+        sc[kTok + lane] = lg2_approx(v < 0x1p-100f ? 0x1p-100f : v);
+        sc[2 * kTok + lane] = rcp_approx(fmaxf(v, 0x1p-100f));
+        __syncwarp();
+      }
       const int t0 = tok0 + i * G::kBlockTok;
       const bool edge = t0 + kTok > all_hi || t0 < all_lo;
 
@@ -444,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 #pragma unroll
               for (int j = 0; j < 4; ++j) qa[mt][j] = qf[kMT == 1 ? ks : 0][j];
             } else {
-              const uint4 t = reinterpret_cast<const uint4*>(smem + SM::kQOff)[(mt * kKS + ks) * 32 + lane];
+              const uint4 t = q_smem[(mt * kKS + ks) * 32];
               qa[mt][0] = t.x; qa[mt][1] = t.y; qa[mt][2] = t.z; qa[mt][3] = t.w;
             }
           }
@@ -471,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 #pragma unroll
                 for (int x = 0; x < 4; ++x) qa[mt][q4][x] = qf[kMT == 1 ? 4 * j + q4 : 0][x];
               } else {
-                const uint4 t = reinterpret_cast<const uint4*>(smem + SM::kQOff)[(mt * kKS + 4 * j + q4) * 32 + lane];
+                const uint4 t = q_smem[(mt * kKS + 4 * j + q4) * 32];
                 qa[mt][q4][0] = t.x; qa[mt][q4][1] = t.y; qa[mt][q4][2] = t.z; qa[mt][q4][3] = t.w;
               }
             }
@@ -489,37 +545,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         }
       }
 
-      // ---- scores in base 2, masks, the value scales' logarithms
+      // ---- scores, masks, the value scales' logarithms.  S becomes z (times the row's factor where it
+      // is not yet applied: bf16 without a cap).
       float inv_vs[kFp8 ? kNT : 1][2];
+      const bool capped = a.softcap > 0.f;
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
         float kf[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
         if (kFp8) {
           const float2 k2 = *reinterpret_cast<const float2*>(sc + nt * 8 + 2 * c);
-          const float2 v2 = *reinterpret_cast<const float2*>(sc + kTok + nt * 8 + 2 * c);
+          const float2 l2 = *reinterpret_cast<const float2*>(sc + kTok + nt * 8 + 2 * c);
+          const float2 i2 = *reinterpret_cast<const float2*>(sc + 2 * kTok + nt * 8 + 2 * c);
           kf[0] = k2.x;
           kf[1] = k2.y;
-          // (a scale that is not a number makes its row of the cache so: kept)
-          const float vx = v2.x < 0x1p-100f ? 0x1p-100f : v2.x, vy = v2.y < 0x1p-100f ? 0x1p-100f : v2.y;
-          lv[0] = lg2_approx(vx);
-          lv[1] = lg2_approx(vy);
-          inv_vs[kFp8 ? nt : 0][0] = rcp_approx(vx);
-          inv_vs[kFp8 ? nt : 0][1] = rcp_approx(vy);
+          lv[0] = l2.x;
+          lv[1] = l2.y;
+          inv_vs[kFp8 ? nt : 0][0] = i2.x;
+          inv_vs[kFp8 ? nt : 0][1] = i2.y;
         }
+        if (capped) {
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
+          for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float z = s[mt][nt][e] * (kFp8 ? kf[e & 1] * rscale[mt][e >> 1] : rscale[mt][e >> 1]);
-            if (a.softcap > 0.f)  // z = cap tanh(z / cap) log2 e
-              z = a.softcap * kLog2e * (1.f - 2.f * rcp_approx(ex2_approx(z * (2.f * kLog2e)) + 1.f));
-            if (kFp8) z += lv[e & 1];
-            if (edge) {
-              const int j = t0 + nt * 8 + 2 * c + (e & 1);
-              if (j >= row_hi[mt][e >> 1] || j < row_lo[mt][e >> 1]) z = -INFINITY;
+            for (int e = 0; e < 4; ++e) {
+              const float z = kFp8 ? s[mt][nt][e] * kf[e & 1] : s[mt][nt][e];
+              s[mt][nt][e] = fmaf(a.softcap * kLog2e, tanh_fast(z * rscale[mt][e >> 1]), lv[e & 1]);
             }
-            s[mt][nt][e] = z;
-          }
+        } else if (kFp8) {
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][nt][e] = fmaf(s[mt][nt][e] * kf[e & 1], rscale[mt][e >> 1], lv[e & 1]);
+        }
+      }
+      if (edge) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = t0 + nt * 8 + 2 * c + (e & 1);
+              if (j >= row_hi[mt][e >> 1] || j < row_lo[mt][e >> 1]) s[mt][nt][e] = -INFINITY;
+            }
       }
       // ---- running maximum and sum; P in place of S
 #pragma unroll
@@ -533,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
           for (int nt = 0; nt < kNT; ++nt) mx = fmaxf(mx, fmaxf(s[mt][nt][2 * x], s[mt][nt][2 * x + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[mt][x], mx);
+          const float fac = kFp8 || capped ? 1.f : rscale[mt][x];
+          const float mn = fmaxf(m[mt][x], mx * fac);
           const float ref = mn == -INFINITY ? 0.f : mn;
           alpha[x] = ex2_approx(m[mt][x] - ref);
           moved |= mn > m[mt][x];
@@ -544,11 +613,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
           for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float z = s[mt][nt][2 * x + e];
-              const float pr = ex2_approx(z - shift);
+              const float pr = ex2_approx(kFp8 ? s[mt][nt][2 * x + e] - shift : fmaf(s[mt][nt][2 * x + e], fac, -shift));
               s[mt][nt][2 * x + e] = pr;
-              if (!kFp8) sum += pr;
-              else if (!(z == -INFINITY)) sum = fmaf(pr, inv_vs[kFp8 ? nt : 0][e], sum);
+              sum = kFp8 ? fmaf(pr, inv_vs[kFp8 ? nt : 0][e], sum) : sum + pr;
             }
           l[mt][x] = l[mt][x] * alpha[x] + sum;
         }
@@ -566,7 +633,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       if (edge) {
         // Rows of V that no query of the unit sees may hold anything (they may never have been
         // written): zero them, since 0 * inf is not 0.
-        bool wrote = false;
         constexpr int kRowChunks = G::kColBlocks * G::kRowBytes / 16;
         auto zero_rows = [&](int r0, int r1) {
           for (int x = r0 * kRowChunks + lane; x < r1 * kRowChunks; x += 32) {
@@ -574,7 +640,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             *reinterpret_cast<uint4*>(st + G::kOpBytes + (ch / (G::kRowBytes / 16)) * (kTok * G::kRowBytes) +
                                       swz<G::kRowBytes>(r, ch % (G::kRowBytes / 16))) = make_uint4(0, 0, 0, 0);
           }
-          wrote |= r1 > r0;
         };
         zero_rows(0, lo - t0);
         zero_rows(max(len - t0, 0), kTok);
@@ -587,7 +652,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             if (r >= low_end && r < all_hi - t0) r = all_hi - t0;
             if (r >= min(len - t0, kTok)) break;
             const int j = t0 + r;
-            constexpr int kChunks = G::kColBlocks * 8;
             uint4* at = reinterpret_cast<uint4*>(st + G::kOpBytes + (lane / 8) * (kTok * 128) + swz<128>(r, lane % 8));
             bool odd = false;
             if (lane < kChunks) {
@@ -620,10 +684,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
               }
             __syncwarp();
             if (lane < kChunks) *at = make_uint4(0, 0, 0, 0);
-            wrote = true;
           }
         }
-        if (wrote) sm100::fence_proxy_async();  // before the next TMA load into this stage
         __syncwarp();
       }
 
@@ -692,106 +754,117 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         }
       }
       __syncwarp();  // the stage has been read
-      done = i + 1;
-      if (++stage_out == G::kStages) {
-        stage_out = 0;
-        phase_out ^= 1;
-      }
+      if (++stage_out == G::kStages) stage_out = 0;
     }
 
-    // ---- the warps' results together
+    // ---- the warps' results together, as a chain: each warp adds its own to the sum that the warp
+    // before it left in shared memory, and the last one writes the result.  A warp that has passed its
+    // sum on goes on with the next unit, whose tiles are under way already.  Barrier w passes the sum
+    // from warp w - 1 to warp w; barrier 4 gives its place back to warp 0.
+    // (a row's four threads hold parts of its sum l)
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 1);
         l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 2);
-        if (c == 0) {
-          s_m[warp * kRows + mt * 16 + x * 8 + g] = m[mt][x];
-          s_l[warp * kRows + mt * 16 + x * 8 + g] = l[mt][x];
+      }
+    if (warp > 0) sm100::named_bar(warp, 64);
+    else if (pieces > 0) sm100::named_bar(4, 64);
+    const bool mine_any = i_begin < i_end, sum_any = warp > 0 && s_any;
+    if (sum_any) {
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt) {
+        const float4 ml = s_ml[mt * 32];
+        float f[2], fs[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float mo = x ? ml.z : ml.x, lo2 = x ? ml.w : ml.y;
+          const float top = fmaxf(m[mt][x], mo);
+          // (a maximum of -inf: no key, or no number; what is added is then 0 or not a number)
+          f[x] = m[mt][x] == -INFINITY ? 1.f : ex2_approx(m[mt][x] - top);
+          fs[x] = mo == -INFINITY ? 1.f : ex2_approx(mo - top);
+          m[mt][x] = top;
+          l[mt][x] = l[mt][x] * f[x] + lo2 * fs[x];
+        }
+#pragma unroll
+        for (int j = 0; j < kDT; ++j) {
+          const float4 t = s_sum[(mt * kDT + j) * 32];
+          o[mt][j][0] = o[mt][j][0] * f[0] + t.x * fs[0];
+          o[mt][j][1] = o[mt][j][1] * f[0] + t.y * fs[0];
+          o[mt][j][2] = o[mt][j][2] * f[1] + t.z * fs[1];
+          o[mt][j][3] = o[mt][j][3] * f[1] + t.w * fs[1];
         }
       }
-    __syncthreads();
-    if (s_abort) {  // a wait ran out: let this warp's copies land (bounded), then leave
-      for (; done < i_issue; ++done) {
-        sm100::mbar_wait(&bars[stage_out], phase_out, kWaitLimitNs);
-        if (++stage_out == G::kStages) {
-          stage_out = 0;
-          phase_out ^= 1;
+    }
+    __syncwarp();  // the sum has been read
+    if (warp < kWarps - 1) {
+      if (mine_any || warp == 0) {
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+          s_ml[mt * 32] = make_float4(m[mt][0], l[mt][0], m[mt][1], l[mt][1]);
+#pragma unroll
+          for (int j = 0; j < kDT; ++j) s_sum[(mt * kDT + j) * 32] = make_float4(o[mt][j][0], o[mt][j][1], o[mt][j][2], o[mt][j][3]);
         }
+        if (lane == 0) s_any = mine_any || sum_any;
       }
-      if (tid == 0) p.meta[cta] = make_int4(0, 0, 0, 0);
-      return;
-    }
-    float* buf = reinterpret_cast<float*>(stages);
+      __syncwarp();
+      sm100::named_bar_arrive(warp + 1, 64);
+    } else {
+      if (more) sm100::named_bar_arrive(4, 64);
+      const bool whole = blk == 0 && take == n_blk;
+      const int64_t slot = 2 * cta + (pieces == 0 ? 0 : 1);
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt)
+      for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int r = mt * 16 + x * 8 + g;
-        float top = -INFINITY;
+        for (int x = 0; x < 2; ++x) {
+          const int r = mt * 16 + x * 8 + g, row = row_base + r;
+          if (row >= p.rows) continue;
+          const float top = m[mt][x], sum = l[mt][x];
+          const int t = row / p.group, head = h * p.group + row - t * p.group;
+          const int64_t at = ((int64_t)b * a.new_tokens + t) * a.hq + head;
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          // this thread's channels: pairs 8 j + 2 c (bf16), or kDT (2 c + y) + j (e4m3)
+          if (!kFp8) {
 #pragma unroll
-        for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_m[v * kRows + r]);
-        const float f = m[mt][x] == -INFINITY ? (l[mt][x] == 0.f ? 0.f : 1.f) : ex2_approx(m[mt][x] - top);
-        if (!kFp8) {
+            for (int j = 0; j < kDT; ++j) {
+              const int ch = 8 * j + 2 * c;
+              if (ch >= a.d) continue;
+              if (whole) *reinterpret_cast<uint32_t*>(a.out + at * a.d + ch) = pack_bf16(o[mt][j][2 * x] * inv, o[mt][j][2 * x + 1] * inv);
+              else *reinterpret_cast<float2*>(p.part_o + (slot * kRows + r) * a.d + ch) = make_float2(o[mt][j][2 * x], o[mt][j][2 * x + 1]);
+            }
+          } else {
 #pragma unroll
-          for (int j = 0; j < kDT; ++j)
-            *reinterpret_cast<float2*>(buf + r * SM::kPitch + 8 * j + 2 * c) = make_float2(o[mt][j][2 * x] * f, o[mt][j][2 * x + 1] * f);
-        } else {
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int j = 0; j < kDT; j += 4)
-              *reinterpret_cast<float4*>(buf + r * SM::kPitch + kDT * (2 * c + y) + j) =
-                  make_float4(o[mt][j][2 * x + y] * f, o[mt][j + 1][2 * x + y] * f, o[mt][j + 2][2 * x + y] * f, o[mt][j + 3][2 * x + y] * f);
+              for (int j = 0; j < kDT; j += 4) {
+                const int ch = kDT * (2 * c + y) + j;
+                if (ch >= a.d) continue;
+                const float v[4] = {o[mt][j][2 * x + y], o[mt][j + 1][2 * x + y], o[mt][j + 2][2 * x + y], o[mt][j + 3][2 * x + y]};
+                if (whole)
+                  *reinterpret_cast<uint2*>(a.out + at * a.d + ch) = make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
+                else
+                  *reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * a.d + ch) = make_float4(v[0], v[1], v[2], v[3]);
+              }
+          }
+          if (c == 0) {
+            if (!whole) p.part_ml[slot * kRows + r] = make_float2(top, sum);
+            else if (a.lse)
+              a.lse[at] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - (kFp8 ? kWeightShift : 0.f) + log2f(sum)) * 0.6931471805599453f;
+          }
         }
-      }
-    __syncthreads();
-    const bool whole = blk == 0 && take == n_blk;
-    const bool head_part = first_part;
-    first_part = false;
-    const int64_t slot = 2 * cta + (head_part ? 0 : 1);
-    const int live = min(kRows, p.rows - row_base);
-    const int d4 = a.d / 4;
-    for (int x = tid; x < live * d4; x += kThreads) {
-      const int r = x / d4, ch = (x - r * d4) * 4;
-      float top = -INFINITY;
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_m[v * kRows + r]);
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
-        const float mv = s_m[v * kRows + r], lv = s_l[v * kRows + r];
-        sum += mv == -INFINITY ? lv : lv * ex2_approx(mv - top);
-        const float4 t = *reinterpret_cast<const float4*>(smem + SM::kStageOff + v * SM::kWarpBytes + (r * SM::kPitch + ch) * 4);
-        acc.x += t.x; acc.y += t.y; acc.z += t.z; acc.w += t.w;
-      }
-      const int row = row_base + r;
-      if (whole) {
-        const int t = row / p.group, head = h * p.group + row - t * p.group;
-        const int64_t at = ((int64_t)b_here * a.new_tokens + t) * a.hq + head;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2*>(a.out + at * a.d + ch) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-        if (ch == 0 && a.lse)
-          a.lse[at] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - (kFp8 ? kWeightShift : 0.f) + log2f(sum)) * 0.6931471805599453f;
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * a.d + ch) = acc;
-        if (ch == 0) p.part_ml[slot * kRows + r] = make_float2(top, sum);
+      if (pieces == 0 && blk > 0 && blk + take == n_blk) {  // this CTA ends a unit that others began
+        // the CTA of its first block; the unit is that CTA's first one if its share begins there, or in
+        // the end (without blocks) of the unit before
+        const int64_t start = w0 - blk;
+        const int64_t c0 = ((start + 1) * ctas - 1) / total;
+        const int64_t first = 2 * c0 + (start - c0 * total / ctas <= kUnitCost ? 0 : 1);
+        meta = make_int4((int)first, (int)(cta - c0 + 1), (int)((int64_t)b * units_per_seq + u), 0);
       }
     }
-    if (head_part && blk > 0 && blk + take == n_blk) {  // this CTA ends a unit that others began
-      // the CTA of its first block; the unit is that CTA's first one if its share begins there, or in
-      // the end (without blocks) of the unit before
-      const int64_t start = w_here - blk;
-      const int64_t c0 = ((start + 1) * ctas - 1) / total;
-      const int64_t first = 2 * c0 + (start - c0 * total / ctas <= kUnitCost ? 0 : 1);
-      meta = make_int4((int)first, (int)(cta - c0 + 1), (int)((int64_t)b_here * units_per_seq + u), 0);
-    }
-    sm100::fence_proxy_async();  // the merge buffers are stages again
-    __syncthreads();
+    ++pieces;
   }
-  if (tid == 0) p.meta[cta] = meta;
+  if (warp == kWarps - 1 && lane == 0) p.meta[cta] = meta;
 }
 
 // Joins the partial results of every unit that more than one CTA worked on, in the order of its
@@ -909,22 +982,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   }
 }
 
-// The cache [pages][heads][page][d] as 4-D (channel, token in page, head, page): boxes of one
-// column block by up to a tile's rows inside one page, zero fill beyond the head size.
-bool make_cache_map(CUtensorMap* map, const void* base, bool fp8, int d, int page, int heads, int pages, int64_t page_stride,
-                    int box_cols, int box_rows) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return false;
-  const cuuint64_t esz = fp8 ? 1 : 2;
-  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)heads, (cuuint64_t)pages};
-  cuuint64_t strides[3] = {d * esz, (cuuint64_t)page * d * esz, (cuuint64_t)page_stride * esz};
-  cuuint32_t box[4] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
-             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols * esz == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Rows of one row block: 16 while all rows of a (sequence, kv head) fit, else 32.
@@ -932,7 +989,7 @@ int rows_per_block(int rows) { return rows <= 16 ? 16 : 32; }
 
 template <bool kFp8, int kDP, int kMT>
 cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
-  using G = Geo<kFp8, kDP>;
+  using G = Geo<kFp8, kDP, kMT>;
   using SM = Smem<kFp8, kDP, kMT>;
   static bool attr_done[64] = {};
   const int sms = sm_count();
@@ -953,16 +1010,10 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   p.meta = reinterpret_cast<int4*>(ws + kWorkspaceHeader);
   p.part_ml = reinterpret_cast<float2*>(ws + kWorkspaceHeader + up256(kMaxCtas * sizeof(int4)));
   p.part_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.part_ml) + up256((size_t)2 * kMaxCtas * SM::kRows * sizeof(float2)));
-  DecodeMaps maps;
-  const int page = 1 << a.page_shift;
-  const int box_rows = page < G::kTok ? page : G::kTok, box_cols = kFp8 ? kDP : 64;
-  if (!make_cache_map(&maps.k, a.k_cache, kFp8, a.d, page, a.hkv, a.num_pages, a.k_page_stride, box_cols, box_rows) ||
-      !make_cache_map(&maps.v, a.v_cache, kFp8, a.d, page, a.hkv, a.num_pages, a.v_page_stride, box_cols, box_rows))
-    return cudaErrorInvalidValue;
   constexpr uint32_t kSmem = SM::kTotal + 1024;
   cudaError_t e = set_smem_once(attn_decode_kernel<kFp8, kDP, kMT>, kSmem, attr_done);
   if (e != cudaSuccess) return e;
-  attn_decode_kernel<kFp8, kDP, kMT><<<(unsigned)grid, kThreads, kSmem, stream>>>(maps, p);
+  attn_decode_kernel<kFp8, kDP, kMT><<<(unsigned)grid, kThreads, kSmem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || most_blocks == 1) return e;  // (no unit has two blocks: nothing to join)
   cudaLaunchConfig_t cfg = {};
