@@ -117,7 +117,7 @@ struct Geo {
   static constexpr int kColBlocks = kFp8 ? 1 : kDP / 64;           // 128-byte column blocks (bf16)
   static constexpr int kOpBytes = kTok * kRowBytes * kColBlocks;   // K (or V) of one tile
   static constexpr int kStageBytes = 2 * kOpBytes;
-  static constexpr int kWarpBytes = kMT == 1 ? 24576 : 16384;
+  static constexpr int kWarpBytes = 16384;
   static constexpr int kStages = kWarpBytes / kStageBytes;
   static constexpr int kBlockTok = kTok * kWarps;
   static constexpr int kScaleBytes = kFp8 ? 3 * kTok * 4 : 0;            // k scales; v scales, then their logarithms; reciprocals
@@ -198,7 +198,8 @@ struct Smem {
   static constexpr int kWarpBytes = G::kWarpBytes;
   static constexpr int kScaleOff = kWarps * kWarpBytes;
   static constexpr int kQOff = kScaleOff + kWarps * G::kStages * G::kScaleBytes;
-  static constexpr int kSumOff = kQOff + 2 * kQFragBytes;                // the warps' sum: [kRows x kDP] floats,
+  static constexpr int kQRowBytes = kMT == 1 ? kRows * kDP * 2 : 0;             // one unit's queries as they are
+  static constexpr int kSumOff = kQOff + 2 * kQFragBytes + 3 * kQRowBytes;      // the warps' sum: [kRows x kDP] floats,
   static constexpr int kMlOff = kSumOff + kRows * kDP * 4;               // and each row's maximum and sum
   static constexpr int kScanOff = kMlOff + kMT * 4 * 32 * 4;             // one int64 per warp
   static constexpr int kTotal = kScanOff + 8 * kWarps;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   // maxima can be taken before it (a factor of zero: zero queries)
   const float base_scale =
       a.scale == 0.f ? 1.f : fmaxf(fabsf(a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e), 1.17549435e-38f);
-  const uint32_t q_sign = a.scale < 0.f ? 0x80008000u : 0u;
+  const uint32_t q_sign = a.scale < 0.f ? 0x80008000u : 0u, q_keep = a.scale == 0.f ? 0u : 0xffffffffu;
 
   // ---- the loading side: a ring of stages, kept full across the units' ends
   constexpr int kChunks = kDP * (kFp8 ? 1 : 2) / 16, kPass = 32 / kChunks;  // 16-byte chunks of a row; rows a pass
@@ -294,13 +295,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   const uint8_t* v_base = static_cast<const uint8_t*>(a.v_cache) + (ld_bytes ? 16 * ld_ch : 0);
   int stage_in = 0, stage_out = 0;
   int in_tok = 0, in_i = 0, in_end = 0, in_h = 0, page_next = 0;
-  bool in_more = true;
+  int in_piece = -1, in_slot = 2, ahead = 0;  // the piece being loaded, its place for queries; tiles under way
+  bool in_more = true, in_first = false;
   // to the next tile; this lane's page is that of the key it stands for (of the nearest key in [lo, len))
   auto advance = [&]() {
     ++in_i;
     while (in_i >= in_end) {
       in_more = in.next(a, units_per_seq);
       if (!in_more) return;
+      ++in_piece;
+      in_slot = in_slot == 2 ? 0 : in_slot + 1;
+      in_first = true;
       in_h = in.u / p.row_blocks;
       in.tiles(warp, kTok, in_tok, in_i, in_end);
     }
@@ -308,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     tok = tok < in.lo ? in.lo : (tok >= in.len ? in.len - 1 : tok);
     page_next = a.page_table[(int64_t)in.b * a.max_pages + (tok >> a.page_shift)];
   };
-  // the copies of the next tile, as one group (empty when there is none left)
+  // the copies of the next tile, as one group
   auto issue = [&]() {
-    if (in_more) {
+    {
       int page = page_next;
       if ((uint32_t)page >= (uint32_t)a.num_pages) {  // never read outside the cache
         if (p.status) atomicOr(p.status, kStatusBadIndex);
@@ -318,6 +323,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
       const int t0 = in_tok + in_i * G::kBlockTok;
       const uint32_t st = ring + stage_in * G::kStageBytes;
+      if (kMT == 1 && in_first) {
+        // the unit's queries come with its first tile: a load that is waited for at the unit's start
+        // would queue behind all the copies under way.  All four warps copy them (the same bytes); of
+        // three places the one behind a warp that lags and before one that leads is free.
+        in_first = false;
+        constexpr int kQChunks = kDP * 2 / 16, kQPass = 32 / kQChunks;
+        const int base = (in.u - in_h * p.row_blocks) * kRows, ch = lane % kQChunks;
+        const int live = min(kRows, p.rows - base);
+        const uint32_t dst = sm100::smem_u32(smem + SM::kQOff + in_slot * SM::kQRowBytes);
+        for (int r = lane / kQChunks; r < live; r += kQPass) {
+          const int t = (base + r) / p.group, head = in_h * p.group + base + r - t * p.group;
+          const __nv_bfloat16* src = a.q + (((int64_t)in.b * a.new_tokens + t) * a.hq + head) * a.d;
+          const bool on = 8 * ch < a.d;
+          cp_async16(dst + r * (kDP * 2) + ((ch ^ (r & 7)) << 4), src + (on ? 8 * ch : 0), on ? 16 : 0);
+        }
+      }
       auto copy_rows = [&](int i, const uint8_t* ks, const uint8_t* vs) {
         const uint32_t row = i * kPass + ld_row;
         const uint32_t dst = st + swz<G::kRowBytes>(row, ld_ch % (G::kRowBytes / 16));
@@ -349,17 +370,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         cp_async4(dst, a.k_scale + s);
         cp_async4(dst + kTok * 4, a.v_scale + s);
       }
-      if (++stage_in == G::kStages) stage_in = 0;
-      advance();
     }
     cp_async_commit();
+    if (++stage_in == G::kStages) stage_in = 0;
+    ++ahead;
+    advance();
   };
   advance();
-#pragma unroll 1
-  for (int k = 0; k < G::kStages - 1; ++k) issue();
 
   int4 meta = make_int4(0, 0, 0, 0);
-  int pieces = 0;
+  int pieces = 0, slot_out = 0;
   bool more = out.next(a, units_per_seq);
   while (more) {
     const int b = out.b, len = out.len, lo = out.lo, blk = out.blk, take = out.take, n_blk = out.n_blk, u = out.u;
@@ -367,90 +387,96 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     int tok0, i_begin, i_end;
     out.tiles(warp, kTok, tok0, i_begin, i_end);
     more = out.next(a, units_per_seq);
-    // ---- the rows' queries as fragments, their key ranges
+
+    // ---- the rows' key ranges, their queries as fragments
     uint4* q_smem = reinterpret_cast<uint4*>(smem + SM::kQOff + (pieces & 1) * SM::kQFragBytes) + lane;
     uint32_t qf[kMT == 1 ? kKS : 1][4];
     float rscale[kMT][2];   // score factor of rows g and g + 8
     int row_hi[kMT][2], row_lo[kMT][2];
+    const __nv_bfloat16* src[kMT][2];
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
-      const __nv_bfloat16* src[2];
+    for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int r = row_base + mt * 16 + s * 8 + g;
         const bool ok = r < p.rows;
-        const bool read = ok && a.scale != 0.f;
         const int t = ok ? r / p.group : 0;
         const int head = h * p.group + (ok ? r - t * p.group : 0);
-        src[s] = read ? a.q + (((int64_t)b * a.new_tokens + t) * a.hq + head) * a.d : nullptr;
+        src[mt][s] = ok ? a.q + (((int64_t)b * a.new_tokens + t) * a.hq + head) * a.d : nullptr;
         const int pos = len - a.new_tokens + t;
         row_hi[mt][s] = ok ? pos + 1 : 0;
         row_lo[mt][s] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
         rscale[mt][s] = base_scale;
       }
-      uint32_t f[kKS][4];
-      if (!kFp8) {
+    auto make_fragments = [&]() {
+      const uint8_t* q_rows = smem + SM::kQOff + slot_out * SM::kQRowBytes;
+      // 8 (4) channels of row tile mt's row 8 s + g
+      auto load16 = [&](int mt, int s, int ch) {
+        if (kMT == 1) return *reinterpret_cast<const uint4*>(q_rows + (8 * s + g) * (kDP * 2) + (((ch / 8) ^ g) << 4));
+        return src[mt][s] && ch < a.d ? __ldg(reinterpret_cast<const uint4*>(src[mt][s] + ch)) : make_uint4(0, 0, 0, 0);
+      };
+      auto load4 = [&](int mt, int s, int ch) {
+        if (kMT == 1) return *reinterpret_cast<const uint32_t*>(q_rows + (8 * s + g) * (kDP * 2) + (((ch / 8) ^ g) << 4) + (ch % 8) * 2);
+        return src[mt][s] && ch < a.d ? __ldg(reinterpret_cast<const unsigned int*>(src[mt][s] + ch)) : 0u;
+      };
 #pragma unroll
-        for (int ks = 0; ks < kKS; ++ks)
+      for (int mt = 0; mt < kMT; ++mt) {
+        uint32_t f[kKS][4];
+        if (!kFp8) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int ch = ks * 16 + (j >> 1) * 8 + 2 * c;
-            f[ks][j] = src[j & 1] && ch < a.d ? __ldg(reinterpret_cast<const unsigned int*>(src[j & 1] + ch)) ^ q_sign : 0u;
+          for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[ks][j] = (load4(mt, j & 1, ks * 16 + (j >> 1) * 8 + 2 * c) & q_keep) ^ q_sign;
+        } else {
+          // channels 64 j + 16 c + 4 s + {0..3} are k-step 4 j + s of this thread (as the key bytes are read)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            uint32_t wv[kDP / 64][8];
+            float big = 0.f;
+#pragma unroll
+            for (int j = 0; j < kDP / 64; ++j) {
+              const uint4 v0 = load16(mt, s, 64 * j + 16 * c), v1 = load16(mt, s, 64 * j + 16 * c + 8);
+              wv[j][0] = v0.x; wv[j][1] = v0.y; wv[j][2] = v0.z; wv[j][3] = v0.w;
+              wv[j][4] = v1.x; wv[j][5] = v1.y; wv[j][6] = v1.z; wv[j][7] = v1.w;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                wv[j][i] = (wv[j][i] & q_keep) ^ q_sign;
+                const float2 t = unpack_bf16(wv[j][i]);
+                big = fmaxf(big, fmaxf(fabsf(t.x), fabsf(t.y)));
+              }
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // the power of two below the row's largest magnitude (exact factors)
+            int e = (int)((__float_as_uint(big) >> 23) & 255) - 127;
+            e = big == 0.f || e > 126 ? 0 : (e < -100 ? -100 : e);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            rscale[mt][s] = base_scale * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int j = 0; j < kDP / 64; ++j)
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4) {
+                const float2 t0 = unpack_bf16(wv[j][2 * q4]), t1 = unpack_bf16(wv[j][2 * q4 + 1]);
+                f[4 * j + q4][s] = pack_half(t0.x * down, t0.y * down);
+                f[4 * j + q4][s + 2] = pack_half(t1.x * down, t1.y * down);
+              }
           }
-      } else {
-        // channels 64 j + 16 c + 4 s + {0..3} are k-step 4 j + s of this thread (as the key bytes are read)
-        float x[2][kDP / 64][16];
-        float big[2] = {0.f, 0.f};
+        }
+        if (kMT == 1) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+          for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
-          for (int j = 0; j < kDP / 64; ++j) {
-            const int ch = 64 * j + 16 * c;
-            uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            if (src[s] && ch < a.d) {
-              v[0] = __ldg(reinterpret_cast<const uint4*>(src[s] + ch));
-              v[1] = __ldg(reinterpret_cast<const uint4*>(src[s] + ch) + 1);
-            }
-            const uint32_t wv[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+            for (int j = 0; j < 4; ++j) qf[kMT == 1 ? ks : 0][j] = f[ks][j];
+        } else {
+          // all four warps write the same; two units' queries alternate, and a warp is at most one unit
+          // ahead of another (the chain of sums below)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 t = unpack_bf16(wv[i] ^ q_sign);
-              x[s][j][2 * i] = t.x;
-              x[s][j][2 * i + 1] = t.y;
-              big[s] = fmaxf(big[s], fmaxf(fabsf(t.x), fabsf(t.y)));
-            }
-          }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          big[s] = fmaxf(big[s], __shfl_xor_sync(0xffffffffu, big[s], 1));
-          big[s] = fmaxf(big[s], __shfl_xor_sync(0xffffffffu, big[s], 2));
-          // the power of two below the row's largest magnitude (exact factors)
-          int e = (int)((__float_as_uint(big[s]) >> 23) & 255) - 127;
-          e = big[s] == 0.f || e > 126 ? 0 : (e < -100 ? -100 : e);
-          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          rscale[mt][s] *= __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-          for (int j = 0; j < kDP / 64; ++j)
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              f[4 * j + q4][s] = pack_half(x[s][j][4 * q4] * down, x[s][j][4 * q4 + 1] * down);
-              f[4 * j + q4][s + 2] = pack_half(x[s][j][4 * q4 + 2] * down, x[s][j][4 * q4 + 3] * down);
-            }
+          for (int ks = 0; ks < kKS; ++ks) q_smem[(mt * kKS + ks) * 32] = make_uint4(f[ks][0], f[ks][1], f[ks][2], f[ks][3]);
         }
       }
-      if (kMT == 1) {
-#pragma unroll
-        for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) qf[kMT == 1 ? ks : 0][j] = f[ks][j];
-      } else {
-        // all four warps write the same; two units' queries alternate, and a warp is at most one unit
-        // ahead of another (the chain of sums below)
-#pragma unroll
-        for (int ks = 0; ks < kKS; ++ks) q_smem[(mt * kKS + ks) * 32] = make_uint4(f[ks][0], f[ks][1], f[ks][2], f[ks][3]);
-      }
-    }
-    if (kMT > 1) __syncwarp();
+      if (kMT > 1) __syncwarp();
+    };
+    if (kMT > 1) make_fragments();
 
     float o[kMT][kDT][4];
     float m[kMT][2], l[kMT][2];
@@ -465,9 +491,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     const int all_hi = len - a.new_tokens + 1, all_lo = a.window > 0 ? len - a.window : 0;
 
     for (int i = i_begin; i < i_end; ++i) {
-      issue();  // into the stage that the tile before has left
-      cp_async_wait<G::kStages - 1>();
+      // refill the stages that the tiles before have left, at most into the next unit
+      while (ahead < G::kStages && in_more && in_piece <= pieces + 1) issue();
+      if (ahead == G::kStages) cp_async_wait<G::kStages - 1>();
+      else if (ahead == 2) cp_async_wait<1>();
+      else if (ahead == 1) cp_async_wait<0>();
+      else cp_async_wait<2>();
       __syncwarp();
+      if (kMT == 1 && i == i_begin) make_fragments();
       uint8_t* st = stages + stage_out * G::kStageBytes;
       const uint32_t ks_addr = sm100::smem_u32(st), vs_addr = ks_addr + G::kOpBytes;
       float* sc = scales + stage_out * 3 * kTok;
@@ -754,13 +785,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         }
       }
       __syncwarp();  // the stage has been read
+      --ahead;
       if (++stage_out == G::kStages) stage_out = 0;
     }
 
     // ---- the warps' results together, as a chain: each warp adds its own to the sum that the warp
     // before it left in shared memory, and the last one writes the result.  A warp that has passed its
     // sum on goes on with the next unit, whose tiles are under way already.  Barrier w passes the sum
-    // from warp w - 1 to warp w; barrier 4 gives its place back to warp 0.
+    // from warp w - 1 to warp w; barrier kWarps gives its place back to warp 0.
     // (a row's four threads hold parts of its sum l)
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt)
@@ -770,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 2);
       }
     if (warp > 0) sm100::named_bar(warp, 64);
-    else if (pieces > 0) sm100::named_bar(4, 64);
+    else if (pieces > 0) sm100::named_bar(kWarps, 64);
     const bool mine_any = i_begin < i_end, sum_any = warp > 0 && s_any;
     if (sum_any) {
 #pragma unroll
@@ -811,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       __syncwarp();
       sm100::named_bar_arrive(warp + 1, 64);
     } else {
-      if (more) sm100::named_bar_arrive(4, 64);
+      if (more) sm100::named_bar_arrive(kWarps, 64);
       const bool whole = blk == 0 && take == n_blk;
       const int64_t slot = 2 * cta + (pieces == 0 ? 0 : 1);
 #pragma unroll
@@ -863,6 +895,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
     }
     ++pieces;
+    slot_out = slot_out == 2 ? 0 : slot_out + 1;
   }
   if (warp == kWarps - 1 && lane == 0) p.meta[cta] = meta;
 }
