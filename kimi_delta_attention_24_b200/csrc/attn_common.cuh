@@ -98,7 +98,7 @@ cudaError_t launch_kv_append(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream);
 // Pieces of work of a norm + rotation call (their count has to stay below 2^31).
-int64_t rope_items(int64_t tokens, int32_t hq, int32_t hk, int32_t hv);
+int64_t rope_items(int64_t tokens, int32_t hq, int32_t hk, int32_t hv, int batches = 1);
 size_t rope_bwd_workspace_bytes();
 size_t attn_decode_workspace_bytes(int32_t rows, int32_t d);
 
