@@ -22,9 +22,9 @@
 //     run far below their rate here (a tile's 48 take ~100 of the ~360 cycles its bytes take).
 //   - bf16 cache: P enters the second product as a bf16 pair hi + lo, so its rounding (2^-17) stays
 //     below that of the bf16 output.  e4m3 cache: codes are exact in fp16; the key's scale multiplies
-//     the score, and the value's enters the exponent, w_j = 2^(z_j + log2 s_j - M) with M the running
-//     maximum of that sum, so w is in (0, 1] whatever the scales are; times 2^14 it is rounded to fp16
-//     (2^-11 down to 2^-28 of the maximum).  q (bf16) is scaled by a power of two per row to fit fp16.
+//     the score, and the value's enters the exponent, w_j = 2^(z_j + log2 s_j - M) with M the row's
+//     reference of that sum (within 2^8 of its maximum), whatever the scales are; times 2^7 it is rounded
+//     to fp16 (2^-11 down to 2^-21 of 2^M).  q (bf16) is scaled by a power of two per row to fit fp16.
 #include <cuda_fp16.h>
 
 #include "attn_common.cuh"
@@ -37,7 +37,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = kCtasPerSm * 160;  // bound used for the workspace (148 SMs on a B200)
-constexpr float kWeightShift = 14.0f;
+constexpr float kLazy = 8.0f;         // how far (base 2) a score passes a row's reference before it moves
+constexpr float kWeightShift = 7.0f;  // fp16 weights: up to 2^(kLazy + kWeightShift) = 2^15
 
 struct DecodeParams {
   AttnDecodeArgs a;
@@ -75,18 +76,19 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 template <bool kHalf>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if (kHalf)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
-  return r;
+// Four e4m3 codes as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   __half2 t = __floats2half2_rn(a, b);
@@ -521,6 +523,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
       if (!kFp8) {
+        constexpr bool kSplit = kNT == 2;
+        float s_odd[kMT][kSplit ? kNT : 1][4] = {};
         const uint32_t mrow = ((lane >> 4) << 3) + (lane & 7), mchunk = (lane >> 3) & 1;
 #pragma unroll
         for (int ks = 0; ks < kKS; ++ks) {
@@ -541,10 +545,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             ldsm4(kb, ks_addr + (ks >> 2) * (kTok * 128) + swz<128>(n2 * 16 + mrow, (ks & 3) * 2 + mchunk));
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt) {
-              mma16816<false>(s[mt][2 * n2], qa[mt], kb[0], kb[1]);
-              mma16816<false>(s[mt][2 * n2 + 1], qa[mt], kb[2], kb[3]);
+              // (one row tile of 16 keys has two sums only: even and odd steps apart, half the chain)
+              float (&s0)[4] = kSplit && (ks & 1) ? s_odd[mt][kSplit ? 2 * n2 : 0] : s[mt][2 * n2];
+              float (&s1)[4] = kSplit && (ks & 1) ? s_odd[mt][kSplit ? 2 * n2 + 1 : 0] : s[mt][2 * n2 + 1];
+              mma16816<false>(s0, qa[mt], kb[0], kb[1]);
+              mma16816<false>(s1, qa[mt], kb[2], kb[3]);
             }
           }
+        }
+        if (kSplit) {
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[mt][nt][e] += s_odd[mt][kSplit ? nt : 0][e];
         }
       } else {
 #pragma unroll
@@ -562,17 +577,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
                 qa[mt][q4][0] = t.x; qa[mt][q4][1] = t.y; qa[mt][q4][2] = t.z; qa[mt][q4][3] = t.w;
               }
             }
+          uint4 kb[kNT];
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            const uint4 kb = *reinterpret_cast<const uint4*>(st + swz<G::kRowBytes>(nt * 8 + g, 4 * j + c));
-            const uint32_t wv[4] = {kb.x, kb.y, kb.z, kb.w};
+          for (int nt = 0; nt < kNT; ++nt) kb[nt] = *reinterpret_cast<const uint4*>(st + swz<G::kRowBytes>(nt * 8 + g, 4 * j + c));
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              const uint32_t b0 = e4m3x2_to_half2(wv[q4]), b1 = e4m3x2_to_half2(wv[q4] >> 16);
+          for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+              uint32_t b0, b1;
+              e4m3x4_to_half2(q4 == 0 ? kb[nt].x : q4 == 1 ? kb[nt].y : q4 == 2 ? kb[nt].z : kb[nt].w, b0, b1);
 #pragma unroll
               for (int mt = 0; mt < kMT; ++mt) mma16816<true>(s[mt][nt], qa[mt][q4], b0, b1);
             }
-          }
         }
       }
 
@@ -620,37 +636,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
               if (j >= row_hi[mt][e >> 1] || j < row_lo[mt][e >> 1]) s[mt][nt][e] = -INFINITY;
             }
       }
-      // ---- running maximum and sum; P in place of S
+      // ---- running sum and reference of the exponents; P in place of S.  The reference m of a row is
+      // its maximum when it was last moved: it moves (for all rows of the warp) only when a score
+      // passes it by kLazy, so P stays below 2^kLazy and most tiles need no exchange between threads.
+      bool passed = false;
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) {
-        float alpha[2];
-        bool moved = false;
+      for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+          const float fac = kFp8 || capped ? 1.f : rscale[mt][x];
           float mx = -INFINITY;
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt) mx = fmaxf(mx, fmaxf(s[mt][nt][2 * x], s[mt][nt][2 * x + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float fac = kFp8 || capped ? 1.f : rscale[mt][x];
-          const float mn = fmaxf(m[mt][x], mx * fac);
-          const float ref = mn == -INFINITY ? 0.f : mn;
-          alpha[x] = ex2_approx(m[mt][x] - ref);
-          moved |= mn > m[mt][x];
-          m[mt][x] = mn;
-          const float shift = kFp8 ? ref - kWeightShift : ref;
-          float sum = 0.f;
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float pr = ex2_approx(kFp8 ? s[mt][nt][2 * x + e] - shift : fmaf(s[mt][nt][2 * x + e], fac, -shift));
-              s[mt][nt][2 * x + e] = pr;
-              sum = kFp8 ? fmaf(pr, inv_vs[kFp8 ? nt : 0][e], sum) : sum + pr;
-            }
-          l[mt][x] = l[mt][x] * alpha[x] + sum;
+          passed |= mx * fac > m[mt][x] + kLazy;
         }
-        if (__any_sync(0xffffffffu, moved)) {
+      if (__any_sync(0xffffffffu, passed)) {
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+          float alpha[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float fac = kFp8 || capped ? 1.f : rscale[mt][x];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) mx = fmaxf(mx, fmaxf(s[mt][nt][2 * x], s[mt][nt][2 * x + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mn = fmaxf(m[mt][x], mx * fac);
+            alpha[x] = ex2_approx(m[mt][x] - (mn == -INFINITY ? 0.f : mn));
+            m[mt][x] = mn;
+            l[mt][x] *= alpha[x];
+          }
 #pragma unroll
           for (int j = 0; j < kDT; ++j) {
             o[mt][j][0] *= alpha[0];
@@ -660,6 +676,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
           }
         }
       }
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float fac = kFp8 || capped ? 1.f : rscale[mt][x];
+          const float shift = (m[mt][x] == -INFINITY ? 0.f : m[mt][x]) - (kFp8 ? kWeightShift : 0.f);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float pr = ex2_approx(kFp8 ? s[mt][nt][2 * x + e] - shift : fmaf(s[mt][nt][2 * x + e], fac, -shift));
+              s[mt][nt][2 * x + e] = pr;
+              l[mt][x] = kFp8 ? fmaf(pr, inv_vs[kFp8 ? nt : 0][e], l[mt][x]) : l[mt][x] + pr;
+            }
+        }
 
       if (edge) {
         // Rows of V that no query of the unit sees may hold anything (they may never have been
@@ -731,17 +762,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               split2(s[mt][2 * kt + (x >> 1)][2 * (x & 1)], s[mt][2 * kt + (x >> 1)][2 * (x & 1) + 1], hi[mt][x], lo2[mt][x]);
+          // (four loads, then their products, hi before lo: a sum is met again after eight others)
 #pragma unroll
-          for (int d2 = 0; d2 < kDT / 2; ++d2) {
-            uint32_t vb[4];
-            ldsm4t(vb, vs_addr + (d2 >> 2) * (kTok * 128) + swz<128>(kt * 16 + vrow, (d2 & 3) * 2 + vchunk));
+          for (int d8 = 0; d8 < kDT / 8; ++d8) {
+            uint32_t vb[4][4];
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-              mma16816<false>(o[mt][2 * d2], hi[mt], vb[0], vb[1]);
-              mma16816<false>(o[mt][2 * d2 + 1], hi[mt], vb[2], vb[3]);
-              mma16816<false>(o[mt][2 * d2], lo2[mt], vb[0], vb[1]);
-              mma16816<false>(o[mt][2 * d2 + 1], lo2[mt], vb[2], vb[3]);
+            for (int q = 0; q < 4; ++q) {
+              const int d2 = 4 * d8 + q;
+              ldsm4t(vb[q], vs_addr + (d2 >> 2) * (kTok * 128) + swz<128>(kt * 16 + vrow, (d2 & 3) * 2 + vchunk));
             }
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt) {
+                  const uint32_t (&pa)[4] = part ? lo2[mt] : hi[mt];
+                  mma16816<false>(o[mt][8 * d8 + 2 * q], pa, vb[q][0], vb[q][1]);
+                  mma16816<false>(o[mt][8 * d8 + 2 * q + 1], pa, vb[q][2], vb[q][3]);
+                }
           }
         }
       } else {
@@ -774,8 +813,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             for (int y = 0; y < 2; ++y) {
               const uint32_t e0 = __byte_perm(vw[0][x], vw[1][x], y ? 0x7362 : 0x5140);
               const uint32_t e1 = __byte_perm(vw[2][x], vw[3][x], y ? 0x7362 : 0x5140);
-              const uint32_t b00 = e4m3x2_to_half2(e0), b10 = e4m3x2_to_half2(e1);
-              const uint32_t b01 = e4m3x2_to_half2(e0 >> 16), b11 = e4m3x2_to_half2(e1 >> 16);
+              uint32_t b00, b01, b10, b11;
+              e4m3x4_to_half2(e0, b00, b01);
+              e4m3x4_to_half2(e1, b10, b11);
 #pragma unroll
               for (int mt = 0; mt < kMT; ++mt) {
                 mma16816<true>(o[mt][4 * x + 2 * y], pa[mt], b00, b10);

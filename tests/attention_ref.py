@@ -121,10 +121,12 @@ def attention(q, k_cache, v_cache, page_table, lens, scale, k_scale=None, v_scal
             rel = 2 * dz + 2.0 ** -20 + (2.0 ** -11 if k_scale is not None else 2.0 ** -16) + 2 * (count + 300) * F32
             dz_l = (p * dz).sum(-1, keepdim=True) / l  # the sum's part of it
             tol = torch.einsum("hgj,jhd->hgd", p * (rel + dz_l), v.abs()) / l
-            # fp16 weights below 2^-14 of 2^14 times the largest are off by up to 2^-25
+            # fp16 weights are p s 2^7 in units of a reference that is at most the largest p s; where they are
+            # subnormal they are off by up to 2^-25, which is 2^-32 of the largest p s, times a code: 2^-32 of the
+            # largest value for each key (l >= 1)
             if k_scale is not None:
                 big = (v.abs().amax((0, 2)))[:, None, None]
-                tol = tol + count * 2.0 ** -38 * big
+                tol = tol + count * 2.0 ** -32 * big
             out[b, t] = o.reshape(hq, d)
             out_tol[b, t] = (BF16 * o.abs() + (1 + BF16) * tol).reshape(hq, d) + 1e-38
             lse[b, t] = (m + torch.log(l)).flatten()
