@@ -8,18 +8,22 @@
 // What bounds it: every key and value row is read once and used by G T rows (G query heads per kv
 // head, T new tokens), 4 G T flops per 2 x 2 bytes (bf16): HBM, until G T is near 64.  So the design
 // is a stream of cache tiles with little else:
-//   - Split: the (sequence, kv head, row block) units are laid end to end as blocks of 4 tiles of
-//     keys, and every CTA (two per SM) takes an equal share of all blocks, wherever it begins and
-//     ends, so ragged lengths cost no balance.  A unit that several CTAs share leaves fp32 partial
-//     results (o, m, l) in the workspace, joined in a fixed order by a second, dependent launch.
-//   - Each of a CTA's 4 warps streams its own tiles (one per block) through its own ring of stages, with
-//     no CTA barrier: 16-byte cp.async copies into swizzled rows (conflict-free matrix loads), kept two
-//     tiles ahead also across the ends of units; about 130 KB of copies in flight per SM.  (TMA boxes
-//     instead cost the issuing warp 800 to 900 cycles a tile, four boxes each, of 2600 to 3400.)
+//   - Split: the (sequence, kv head, row block) units are laid end to end as blocks of one tile of keys
+//     per warp, and every CTA (two or three per SM) takes an equal share of all blocks, wherever it
+//     begins and ends, so ragged lengths cost no balance.  A unit that several CTAs share leaves fp32
+//     partial results (o, m, l) in the workspace, joined in a fixed order by a second, dependent launch.
+//   - Each of a CTA's warps streams its own tiles (one per block) through its own ring of stages, with
+//     no CTA barrier: 16-byte cp.async copies into swizzled rows (conflict-free matrix loads), under way
+//     also across the ends of units; about 130 KB of copies in flight per SM.  (TMA boxes instead cost
+//     the issuing warp 800 to 900 cycles a tile, four boxes each, of 2600 to 3400.)
 //   - The warps' results of a unit meet as a chain through shared memory, so that no warp waits for a
 //     slower one before it goes on with the next unit.
-//   - Up to 16 rows (32 where a unit has more) form one mma.sync m16n8k16 operand; these instructions
-//     run far below their rate here (a tile's 48 take ~100 of the ~360 cycles its bytes take).
+//   - The products are transposed, S^T = K Q^T and O^T = V^T P^T, mma.sync m16n8k16 with the keys (the
+//     channels) as the 16 and 8 rows of queries as the 8: a unit of up to 8 rows (one kv head's group
+//     at T = 1) wastes half as much of each instruction, and half the registers, as with 16 rows.
+//   - What remains to be hidden is latency: two warps per scheduler took 2600 to 3400 cycles a tile
+//     whether its bytes had arrived or not.  So dependent products are kept apart, and the softmax
+//     exchanges maxima between threads only when a score passes its row's reference by 2^8.
 //   - bf16 cache: P enters the second product as a bf16 pair hi + lo, so its rounding (2^-17) stays
 //     below that of the bf16 output.  e4m3 cache: codes are exact in fp16; the key's scale multiplies
 //     the score, and the value's enters the exponent, w_j = 2^(z_j + log2 s_j - M) with M the row's
@@ -33,18 +37,15 @@
 namespace kda {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kCtasPerSm = 2;
-constexpr int kMaxCtas = kCtasPerSm * 160;  // bound used for the workspace (148 SMs on a B200)
+constexpr int kMaxCtas = 3 * 160;     // bound used for the workspace (148 SMs on a B200)
 constexpr float kLazy = 8.0f;         // how far (base 2) a score passes a row's reference before it moves
 constexpr float kWeightShift = 7.0f;  // fp16 weights: up to 2^(kLazy + kWeightShift) = 2^15
 
 struct DecodeParams {
   AttnDecodeArgs a;
   int32_t group, rows, row_blocks;  // rows = new_tokens * group, of one (sequence, kv head)
-  float* part_o;                    // [2 * CTAs][rows per block][d]
-  float2* part_ml;                  // [2 * CTAs][rows per block]
+  float4* part_o;                   // [2 * CTAs][row tile][channel tile][lane]: as the product leaves it
+  float4* part_ml;                  // [2 * CTAs][row tile][lane]: (m, l) of the lane's two rows
   int4* meta;                       // [CTAs]: first partial, partials, unit, 0
   uint32_t* status;
 };
@@ -72,6 +73,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// An 8 x 8 matrix of 16-bit elements transposed among the lanes (lane: row lane / 4, columns 2 (lane % 4) + {0, 1}).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 template <bool kHalf>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -110,10 +117,14 @@ __device__ __forceinline__ float tanh_fast(float x) {
 }
 
 // Tile geometry.  kDP: the head size padded to 64 or 128 channels (the padding is zero in q and in
-// the loaded rows); kTok: keys of one warp's tile, 8 KB of K and V together (4 KB for 64 e4m3
-// channels); a block is one tile per warp.
-template <bool kFp8, int kDP, int kMT>
+// the loaded rows); kNQ: tiles of 8 rows per unit; kTok: keys of one warp's tile, 8 KB of K and V
+// together (4 KB for 64 e4m3 channels); a block is one tile per warp.  Up to 8 rows the registers
+// (168 a thread) leave room for 12 warps per SM, else (255) for 8.
+template <bool kFp8, int kDP, int kNQ>
 struct Geo {
+  static constexpr int kWarps = kNQ == 1 && kFp8 ? 6 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCtasPerSm = kNQ == 1 && !kFp8 ? 3 : 2;
   static constexpr int kTok = kFp8 ? 32 : (kDP == 128 ? 16 : 32);
   static constexpr int kRowBytes = kFp8 ? kDP : 128;               // bytes of a row in one column block
   static constexpr int kColBlocks = kFp8 ? 1 : kDP / 64;           // 128-byte column blocks (bf16)
@@ -122,7 +133,7 @@ struct Geo {
   static constexpr int kWarpBytes = 16384;
   static constexpr int kStages = kWarpBytes / kStageBytes;
   static constexpr int kBlockTok = kTok * kWarps;
-  static constexpr int kScaleBytes = kFp8 ? 3 * kTok * 4 : 0;            // k scales; v scales, then their logarithms; reciprocals
+  static constexpr int kScaleBytes = kFp8 ? 3 * kTok * 4 : 0;      // k scales; v scales, then their logarithms; reciprocals
 };
 
 // Byte offset of 16-byte chunk `chunk` of row `row` in a swizzled block of kRowBytes-wide rows.
@@ -191,32 +202,50 @@ struct Walk {
   }
 };
 
-template <bool kFp8, int kDP, int kMT>
+template <bool kFp8, int kDP, int kNQ>
 struct Smem {
-  using G = Geo<kFp8, kDP, kMT>;
-  static constexpr int kRows = 16 * kMT;
-  static constexpr int kQFragBytes = kMT > 1 ? kMT * (kDP / 16) * 32 * 16 : 0;  // one unit's queries
-  static constexpr int kStageOff = 0;
-  static constexpr int kWarpBytes = G::kWarpBytes;
-  static constexpr int kScaleOff = kWarps * kWarpBytes;
-  static constexpr int kQOff = kScaleOff + kWarps * G::kStages * G::kScaleBytes;
-  static constexpr int kQRowBytes = kMT == 1 ? kRows * kDP * 2 : 0;             // one unit's queries as they are
-  static constexpr int kSumOff = kQOff + 2 * kQFragBytes + 3 * kQRowBytes;      // the warps' sum: [kRows x kDP] floats,
-  static constexpr int kMlOff = kSumOff + kRows * kDP * 4;               // and each row's maximum and sum
-  static constexpr int kScanOff = kMlOff + kMT * 4 * 32 * 4;             // one int64 per warp
-  static constexpr int kTotal = kScanOff + 8 * kWarps;
+  using G = Geo<kFp8, kDP, kNQ>;
+  static constexpr int kRows = 8 * kNQ, kDM = kDP / 16;
+  static constexpr bool kQRegs = kNQ <= 2;                                            // query fragments in registers
+  static constexpr int kQFragBytes = kQRegs ? 0 : kNQ * (kDP / 16) * 32 * 8;          // else here: one unit's
+  static constexpr int kQRowBytes = kQRegs ? kRows * kDP * 2 : 0;                     // one unit's queries as they are
+  static constexpr int kScaleOff = G::kWarps * G::kWarpBytes;                         // (the rings come first)
+  static constexpr int kQOff = kScaleOff + G::kWarps * G::kStages * G::kScaleBytes;
+  static constexpr int kSumOff = kQOff + 2 * kQFragBytes + 3 * kQRowBytes;            // the warps' sum,
+  static constexpr int kMlOff = kSumOff + kNQ * kDM * 32 * 16;                        // and each row's maximum and sum
+  static constexpr int kScanOff = kMlOff + kNQ * 32 * 16;                             // one int64 per warp
+  static constexpr int kTotal = kScanOff + 8 * G::kWarps;
 };
 
-template <bool kFp8, int kDP, int kMT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
-  using G = Geo<kFp8, kDP, kMT>;
-  using SM = Smem<kFp8, kDP, kMT>;
-  constexpr int kTok = G::kTok, kNT = kTok / 8, kKS = kDP / 16, kDT = kDP / 8, kRows = SM::kRows;
+// Rows of one row tile (o / l) to the output: o[jj] as the product leaves it, channel tile jj, the
+// lane's rows 2 c + {0, 1}; inv their 1 / l.  row_out: the output row of tile row lane / 4, or null.
+template <bool kFp8, int kDP>
+__device__ __forceinline__ void write_tile(const float (&o)[4], int jj, const float (&inv)[2], __nv_bfloat16* row_out, int d) {
+  const int c = threadIdx.x & 3;
+  // after the transposition a lane holds two channels of row lane / 4
+  const uint32_t t0 = transpose8(pack_bf16(o[0] * inv[0], o[1] * inv[1]));
+  const uint32_t t1 = transpose8(pack_bf16(o[2] * inv[0], o[3] * inv[1]));
+  // bf16: channels 16 jj + 2 c + {0, 1}, and 8 further; e4m3: (kDP / 8) (2 c) + 2 jj and (kDP / 8) (2 c + 1) + 2 jj, each with the next
+  const int ch0 = kFp8 ? (kDP / 8) * 2 * c + 2 * jj : 16 * jj + 2 * c, ch1 = ch0 + (kFp8 ? kDP / 8 : 8);
+  if (row_out && ch0 < d) *reinterpret_cast<uint32_t*>(row_out + ch0) = kFp8 ? __byte_perm(t0, t1, 0x5410) : t0;
+  if (row_out && ch1 < d) *reinterpret_cast<uint32_t*>(row_out + ch1) = kFp8 ? __byte_perm(t0, t1, 0x7632) : t1;
+}
+__device__ __forceinline__ float lse_of(float m, float l, float shift) {
+  return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) - shift + log2f(l)) * 0.6931471805599453f;
+}
+
+template <bool kFp8, int kDP, int kNQ>
+__global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ>::kThreads, Geo<kFp8, kDP, kNQ>::kCtasPerSm)
+    attn_decode_kernel(const __grid_constant__ DecodeParams p) {
+  using G = Geo<kFp8, kDP, kNQ>;
+  using SM = Smem<kFp8, kDP, kNQ>;
+  constexpr int kWarps = G::kWarps, kThreads = G::kThreads;
+  constexpr int kTok = G::kTok, kKT = kTok / 16, kKS = kDP / 16, kDM = SM::kDM, kRows = SM::kRows;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (sm100::smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* smem = smem_raw + ((128 - (sm100::smem_u32(smem_raw) & 127)) & 127);
   const AttnDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  uint8_t* stages = smem + SM::kStageOff + warp * SM::kWarpBytes;
+  uint8_t* stages = smem + warp * G::kWarpBytes;
   float* scales = reinterpret_cast<float*>(smem + SM::kScaleOff) + warp * G::kStages * (G::kScaleBytes / 4);
   float4* s_sum = reinterpret_cast<float4*>(smem + SM::kSumOff) + lane;
   float4* s_ml = reinterpret_cast<float4*>(smem + SM::kMlOff) + lane;
@@ -325,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
       const int t0 = in_tok + in_i * G::kBlockTok;
       const uint32_t st = ring + stage_in * G::kStageBytes;
-      if (kMT == 1 && in_first) {
+      if (SM::kQRegs && in_first) {
         // the unit's queries come with its first tile: a load that is waited for at the unit's start
         // would queue behind all the copies under way.  All four warps copy them (the same bytes); of
         // three places the one behind a warp that lags and before one that leads is free.
@@ -390,104 +419,108 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     out.tiles(warp, kTok, tok0, i_begin, i_end);
     more = out.next(a, units_per_seq);
 
-    // ---- the rows' key ranges, their queries as fragments
-    uint4* q_smem = reinterpret_cast<uint4*>(smem + SM::kQOff + (pieces & 1) * SM::kQFragBytes) + lane;
-    uint32_t qf[kMT == 1 ? kKS : 1][4];
-    float rscale[kMT][2];   // score factor of rows g and g + 8
-    int row_hi[kMT][2], row_lo[kMT][2];
-    const __nv_bfloat16* src[kMT][2];
+    // ---- the rows' key ranges, their queries as fragments.  A lane works on the scores of rows
+    // 2 c + {0, 1} of each row tile, and holds the queries of row g.
+    uint2* q_smem = reinterpret_cast<uint2*>(smem + SM::kQOff + (pieces & 1) * SM::kQFragBytes) + lane;
+    uint32_t qf[SM::kQRegs ? kNQ : 1][SM::kQRegs ? kKS : 1][2];
+    float rscale[kNQ][2];   // score factor of the lane's rows
+    int row_hi[kNQ][2], row_lo[kNQ][2];
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt)
+    for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int r = row_base + mt * 16 + s * 8 + g;
-        const bool ok = r < p.rows;
-        const int t = ok ? r / p.group : 0;
-        const int head = h * p.group + (ok ? r - t * p.group : 0);
-        src[mt][s] = ok ? a.q + (((int64_t)b * a.new_tokens + t) * a.hq + head) * a.d : nullptr;
-        const int pos = len - a.new_tokens + t;
-        row_hi[mt][s] = ok ? pos + 1 : 0;
-        row_lo[mt][s] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-        rscale[mt][s] = base_scale;
+      for (int x = 0; x < 2; ++x) {
+        const int r = row_base + nq * 8 + 2 * c + x;
+        const int pos = len - a.new_tokens + r / p.group;
+        row_hi[nq][x] = r < p.rows ? pos + 1 : 0;
+        row_lo[nq][x] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+        rscale[nq][x] = base_scale;
       }
     auto make_fragments = [&]() {
       const uint8_t* q_rows = smem + SM::kQOff + slot_out * SM::kQRowBytes;
-      // 8 (4) channels of row tile mt's row 8 s + g
-      auto load16 = [&](int mt, int s, int ch) {
-        if (kMT == 1) return *reinterpret_cast<const uint4*>(q_rows + (8 * s + g) * (kDP * 2) + (((ch / 8) ^ g) << 4));
-        return src[mt][s] && ch < a.d ? __ldg(reinterpret_cast<const uint4*>(src[mt][s] + ch)) : make_uint4(0, 0, 0, 0);
-      };
-      auto load4 = [&](int mt, int s, int ch) {
-        if (kMT == 1) return *reinterpret_cast<const uint32_t*>(q_rows + (8 * s + g) * (kDP * 2) + (((ch / 8) ^ g) << 4) + (ch % 8) * 2);
-        return src[mt][s] && ch < a.d ? __ldg(reinterpret_cast<const unsigned int*>(src[mt][s] + ch)) : 0u;
-      };
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) {
-        uint32_t f[kKS][4];
+      for (int nq = 0; nq < kNQ; ++nq) {
+        const __nv_bfloat16* src = nullptr;
+        if (!SM::kQRegs) {
+          const int r = row_base + nq * 8 + g;
+          const int t = r / p.group, head = h * p.group + r - t * p.group;
+          if (r < p.rows) src = a.q + (((int64_t)b * a.new_tokens + t) * a.hq + head) * a.d;
+        }
+        // `ch` .. of row g, as they are in the ring or in global memory
+        auto load16 = [&](int ch) {
+          if (SM::kQRegs) return *reinterpret_cast<const uint4*>(q_rows + (8 * nq + g) * (kDP * 2) + (((ch / 8) ^ g) << 4));
+          return src && ch < a.d ? __ldg(reinterpret_cast<const uint4*>(src + ch)) : make_uint4(0, 0, 0, 0);
+        };
+        auto load4 = [&](int ch) {
+          if (SM::kQRegs) return *reinterpret_cast<const uint32_t*>(q_rows + (8 * nq + g) * (kDP * 2) + (((ch / 8) ^ g) << 4) + (ch % 8) * 2);
+          return src && ch < a.d ? __ldg(reinterpret_cast<const unsigned int*>(src + ch)) : 0u;
+        };
+        uint32_t f[kKS][2];
         if (!kFp8) {
 #pragma unroll
-          for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[ks][j] = (load4(mt, j & 1, ks * 16 + (j >> 1) * 8 + 2 * c) & q_keep) ^ q_sign;
+          for (int ks = 0; ks < kKS; ++ks) {
+            f[ks][0] = (load4(16 * ks + 2 * c) & q_keep) ^ q_sign;
+            f[ks][1] = (load4(16 * ks + 8 + 2 * c) & q_keep) ^ q_sign;
+          }
         } else {
-          // channels 64 j + 16 c + 4 s + {0..3} are k-step 4 j + s of this thread (as the key bytes are read)
+          // channels 64 j + 16 c + 4 s + {0..3} are k-step 4 j + s of this lane (as the key bytes are read)
+          uint32_t wv[kDP / 64][8];
+          float big = 0.f;
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            uint32_t wv[kDP / 64][8];
-            float big = 0.f;
+          for (int j = 0; j < kDP / 64; ++j) {
+            const uint4 v0 = load16(64 * j + 16 * c), v1 = load16(64 * j + 16 * c + 8);
+            wv[j][0] = v0.x; wv[j][1] = v0.y; wv[j][2] = v0.z; wv[j][3] = v0.w;
+            wv[j][4] = v1.x; wv[j][5] = v1.y; wv[j][6] = v1.z; wv[j][7] = v1.w;
 #pragma unroll
-            for (int j = 0; j < kDP / 64; ++j) {
-              const uint4 v0 = load16(mt, s, 64 * j + 16 * c), v1 = load16(mt, s, 64 * j + 16 * c + 8);
-              wv[j][0] = v0.x; wv[j][1] = v0.y; wv[j][2] = v0.z; wv[j][3] = v0.w;
-              wv[j][4] = v1.x; wv[j][5] = v1.y; wv[j][6] = v1.z; wv[j][7] = v1.w;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                wv[j][i] = (wv[j][i] & q_keep) ^ q_sign;
-                const float2 t = unpack_bf16(wv[j][i]);
-                big = fmaxf(big, fmaxf(fabsf(t.x), fabsf(t.y)));
-              }
+            for (int i = 0; i < 8; ++i) {
+              wv[j][i] = (wv[j][i] & q_keep) ^ q_sign;
+              const float2 t = unpack_bf16(wv[j][i]);
+              big = fmaxf(big, fmaxf(fabsf(t.x), fabsf(t.y)));
             }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // the power of two below the row's largest magnitude (exact factors)
-            int e = (int)((__float_as_uint(big) >> 23) & 255) - 127;
-            e = big == 0.f || e > 126 ? 0 : (e < -100 ? -100 : e);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            rscale[mt][s] = base_scale * __uint_as_float((uint32_t)(127 + e) << 23);
+          }
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          // the power of two below the row's largest magnitude (exact factors)
+          int e = (int)((__float_as_uint(big) >> 23) & 255) - 127;
+          e = big == 0.f || e > 126 ? 0 : (e < -100 ? -100 : e);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-            for (int j = 0; j < kDP / 64; ++j)
+          for (int x = 0; x < 2; ++x) rscale[nq][x] = base_scale * __shfl_sync(0xffffffffu, up, 4 * (2 * c + x));
 #pragma unroll
-              for (int q4 = 0; q4 < 4; ++q4) {
-                const float2 t0 = unpack_bf16(wv[j][2 * q4]), t1 = unpack_bf16(wv[j][2 * q4 + 1]);
-                f[4 * j + q4][s] = pack_half(t0.x * down, t0.y * down);
-                f[4 * j + q4][s + 2] = pack_half(t1.x * down, t1.y * down);
-              }
+          for (int j = 0; j < kDP / 64; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 t = unpack_bf16(wv[j][i]);
+              f[4 * j + i / 2][i & 1] = pack_half(t.x * down, t.y * down);
+            }
+        }
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks) {
+          if (SM::kQRegs) {
+            qf[SM::kQRegs ? nq : 0][SM::kQRegs ? ks : 0][0] = f[ks][0];
+            qf[SM::kQRegs ? nq : 0][SM::kQRegs ? ks : 0][1] = f[ks][1];
+          } else {
+            // all warps write the same; two units' queries alternate, and a warp is at most one unit
+            // ahead of another (the chain of sums below)
+            q_smem[(nq * kKS + ks) * 32] = make_uint2(f[ks][0], f[ks][1]);
           }
         }
-        if (kMT == 1) {
-#pragma unroll
-          for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) qf[kMT == 1 ? ks : 0][j] = f[ks][j];
-        } else {
-          // all four warps write the same; two units' queries alternate, and a warp is at most one unit
-          // ahead of another (the chain of sums below)
-#pragma unroll
-          for (int ks = 0; ks < kKS; ++ks) q_smem[(mt * kKS + ks) * 32] = make_uint4(f[ks][0], f[ks][1], f[ks][2], f[ks][3]);
-        }
       }
-      if (kMT > 1) __syncwarp();
+      if (!SM::kQRegs) __syncwarp();
     };
-    if (kMT > 1) make_fragments();
+    if (!SM::kQRegs) make_fragments();
+    auto query = [&](int nq, int ks) {
+      if (SM::kQRegs) return make_uint2(qf[SM::kQRegs ? nq : 0][SM::kQRegs ? ks : 0][0], qf[SM::kQRegs ? nq : 0][SM::kQRegs ? ks : 0][1]);
+      return q_smem[(nq * kKS + ks) * 32];
+    };
 
-    float o[kMT][kDT][4];
-    float m[kMT][2], l[kMT][2];
+    float o[kNQ][kDM][4];         // O^T: rows 2 c + (e & 1); channels 16 jj + g + 8 (e >> 1), or (kDP / 8) g + 2 jj + (e >> 1) (e4m3)
+    float m[kNQ][2], l[kNQ][2];
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
+    for (int nq = 0; nq < kNQ; ++nq) {
 #pragma unroll
-      for (int j = 0; j < kDT; ++j) o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.f;
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.f;
+      for (int j = 0; j < kDM; ++j) o[nq][j][0] = o[nq][j][1] = o[nq][j][2] = o[nq][j][3] = 0.f;
+      m[nq][0] = m[nq][1] = -INFINITY;
+      l[nq][0] = l[nq][1] = 0.f;
     }
     // tiles whose every key every row sees need no mask
     const int all_hi = len - a.new_tokens + 1, all_lo = a.window > 0 ? len - a.window : 0;
@@ -500,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       else if (ahead == 1) cp_async_wait<0>();
       else cp_async_wait<2>();
       __syncwarp();
-      if (kMT == 1 && i == i_begin) make_fragments();
+      if (SM::kQRegs && i == i_begin) make_fragments();
       uint8_t* st = stages + stage_out * G::kStageBytes;
       const uint32_t ks_addr = sm100::smem_u32(st), vs_addr = ks_addr + G::kOpBytes;
       float* sc = scales + stage_out * 3 * kTok;
@@ -516,179 +549,149 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       const int t0 = tok0 + i * G::kBlockTok;
       const bool edge = t0 + kTok > all_hi || t0 < all_lo;
 
-      // ---- S = Q K^T
-      float s[kMT][kNT][4];
-#pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+      // ---- S^T = K Q^T: element e of s[kt][nq] is key 16 kt + g + 8 (e >> 1), row 2 c + (e & 1).
+      // Few sums are kept in several parts, so that a product does not wait for the one before.
+      constexpr int kParts = kKT * kNQ == 1 ? 4 : kKT * kNQ == 2 ? 2 : 1;
+      float sp[kParts][kKT][kNQ][4] = {};
       if (!kFp8) {
-        constexpr bool kSplit = kNT == 2;
-        float s_odd[kMT][kSplit ? kNT : 1][4] = {};
-        const uint32_t mrow = ((lane >> 4) << 3) + (lane & 7), mchunk = (lane >> 3) & 1;
+        const uint32_t mrow = (((lane >> 3) & 1) << 3) + (lane & 7), mchunk = lane >> 4;
 #pragma unroll
-        for (int ks = 0; ks < kKS; ++ks) {
-          uint32_t qa[kMT][4];
+        for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-            if (kMT == 1) {
+          for (int kt = 0; kt < kKT; ++kt) {
+            uint32_t ka[4];
+            ldsm4(ka, ks_addr + (ks >> 2) * (kTok * 128) + swz<128>(kt * 16 + mrow, (ks & 3) * 2 + mchunk));
 #pragma unroll
-              for (int j = 0; j < 4; ++j) qa[mt][j] = qf[kMT == 1 ? ks : 0][j];
-            } else {
-              const uint4 t = q_smem[(mt * kKS + ks) * 32];
-              qa[mt][0] = t.x; qa[mt][1] = t.y; qa[mt][2] = t.z; qa[mt][3] = t.w;
+            for (int nq = 0; nq < kNQ; ++nq) {
+              const uint2 q = query(nq, ks);
+              mma16816<false>(sp[ks % kParts][kt][nq], ka, q.x, q.y);
             }
           }
-#pragma unroll
-          for (int n2 = 0; n2 < kNT / 2; ++n2) {
-            uint32_t kb[4];
-            ldsm4(kb, ks_addr + (ks >> 2) * (kTok * 128) + swz<128>(n2 * 16 + mrow, (ks & 3) * 2 + mchunk));
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-              // (one row tile of 16 keys has two sums only: even and odd steps apart, half the chain)
-              float (&s0)[4] = kSplit && (ks & 1) ? s_odd[mt][kSplit ? 2 * n2 : 0] : s[mt][2 * n2];
-              float (&s1)[4] = kSplit && (ks & 1) ? s_odd[mt][kSplit ? 2 * n2 + 1 : 0] : s[mt][2 * n2 + 1];
-              mma16816<false>(s0, qa[mt], kb[0], kb[1]);
-              mma16816<false>(s1, qa[mt], kb[2], kb[3]);
-            }
-          }
-        }
-        if (kSplit) {
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[mt][nt][e] += s_odd[mt][kSplit ? nt : 0][e];
-        }
       } else {
 #pragma unroll
         for (int j = 0; j < kDP / 64; ++j) {
-          uint32_t qa[kMT][4][4];
+          uint4 kb[kKT][2];
 #pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
+          for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              if (kMT == 1) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) qa[mt][q4][x] = qf[kMT == 1 ? 4 * j + q4 : 0][x];
-              } else {
-                const uint4 t = q_smem[(mt * kKS + 4 * j + q4) * 32];
-                qa[mt][q4][0] = t.x; qa[mt][q4][1] = t.y; qa[mt][q4][2] = t.z; qa[mt][q4][3] = t.w;
-              }
-            }
-          uint4 kb[kNT];
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) kb[nt] = *reinterpret_cast<const uint4*>(st + swz<G::kRowBytes>(nt * 8 + g, 4 * j + c));
+            for (int x = 0; x < 2; ++x) kb[kt][x] = *reinterpret_cast<const uint4*>(st + swz<G::kRowBytes>(kt * 16 + 8 * x + g, 4 * j + c));
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4)
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
-              uint32_t b0, b1;
-              e4m3x4_to_half2(q4 == 0 ? kb[nt].x : q4 == 1 ? kb[nt].y : q4 == 2 ? kb[nt].z : kb[nt].w, b0, b1);
+            for (int kt = 0; kt < kKT; ++kt) {
+              auto word = [&](int x) { return q4 == 0 ? kb[kt][x].x : q4 == 1 ? kb[kt][x].y : q4 == 2 ? kb[kt][x].z : kb[kt][x].w; };
+              uint32_t ka[4];
+              e4m3x4_to_half2(word(0), ka[0], ka[2]);
+              e4m3x4_to_half2(word(1), ka[1], ka[3]);
 #pragma unroll
-              for (int mt = 0; mt < kMT; ++mt) mma16816<true>(s[mt][nt], qa[mt][q4], b0, b1);
+              for (int nq = 0; nq < kNQ; ++nq) {
+                const uint2 q = query(nq, 4 * j + q4);
+                mma16816<true>(sp[q4 % kParts][kt][nq], ka, q.x, q.y);
+              }
             }
         }
       }
+      float (&s)[kKT][kNQ][4] = sp[0];
+#pragma unroll
+      for (int part = 1; part < kParts; ++part)
+#pragma unroll
+        for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+          for (int nq = 0; nq < kNQ; ++nq)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[kt][nq][e] += sp[part][kt][nq][e];
 
       // ---- scores, masks, the value scales' logarithms.  S becomes z (times the row's factor where it
       // is not yet applied: bf16 without a cap).
-      float inv_vs[kFp8 ? kNT : 1][2];
+      float inv_vs[kFp8 ? kKT : 1][2];
       const bool capped = a.softcap > 0.f;
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
+      for (int kt = 0; kt < kKT; ++kt) {
         float kf[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
         if (kFp8) {
-          const float2 k2 = *reinterpret_cast<const float2*>(sc + nt * 8 + 2 * c);
-          const float2 l2 = *reinterpret_cast<const float2*>(sc + kTok + nt * 8 + 2 * c);
-          const float2 i2 = *reinterpret_cast<const float2*>(sc + 2 * kTok + nt * 8 + 2 * c);
-          kf[0] = k2.x;
-          kf[1] = k2.y;
-          lv[0] = l2.x;
-          lv[1] = l2.y;
-          inv_vs[kFp8 ? nt : 0][0] = i2.x;
-          inv_vs[kFp8 ? nt : 0][1] = i2.y;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int key = kt * 16 + g + 8 * y;
+            kf[y] = sc[key];
+            lv[y] = sc[kTok + key];
+            inv_vs[kFp8 ? kt : 0][y] = sc[2 * kTok + key];
+          }
         }
         if (capped) {
 #pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
+          for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float z = kFp8 ? s[mt][nt][e] * kf[e & 1] : s[mt][nt][e];
-              s[mt][nt][e] = fmaf(a.softcap * kLog2e, tanh_fast(z * rscale[mt][e >> 1]), lv[e & 1]);
+              const float z = kFp8 ? s[kt][nq][e] * kf[e >> 1] : s[kt][nq][e];
+              s[kt][nq][e] = fmaf(a.softcap * kLog2e, tanh_fast(z * rscale[nq][e & 1]), lv[e >> 1]);
             }
         } else if (kFp8) {
 #pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
+          for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][nt][e] = fmaf(s[mt][nt][e] * kf[e & 1], rscale[mt][e >> 1], lv[e & 1]);
+            for (int e = 0; e < 4; ++e) s[kt][nq][e] = fmaf(s[kt][nq][e] * kf[e >> 1], rscale[nq][e & 1], lv[e >> 1]);
         }
       }
       if (edge) {
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
+        for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
+          for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int j = t0 + nt * 8 + 2 * c + (e & 1);
-              if (j >= row_hi[mt][e >> 1] || j < row_lo[mt][e >> 1]) s[mt][nt][e] = -INFINITY;
+              const int j = t0 + kt * 16 + g + 8 * (e >> 1);
+              if (j >= row_hi[nq][e & 1] || j < row_lo[nq][e & 1]) s[kt][nq][e] = -INFINITY;
             }
       }
       // ---- running sum and reference of the exponents; P in place of S.  The reference m of a row is
       // its maximum when it was last moved: it moves (for all rows of the warp) only when a score
-      // passes it by kLazy, so P stays below 2^kLazy and most tiles need no exchange between threads.
+      // passes it by kLazy, so P stays below 2^kLazy and most tiles need no exchange between lanes.
+      float mx[kNQ][2];
       bool passed = false;
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
+      for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float fac = kFp8 || capped ? 1.f : rscale[mt][x];
-          float mx = -INFINITY;
+          mx[nq][x] = -INFINITY;
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) mx = fmaxf(mx, fmaxf(s[mt][nt][2 * x], s[mt][nt][2 * x + 1]));
-          passed |= mx * fac > m[mt][x] + kLazy;
+          for (int kt = 0; kt < kKT; ++kt) mx[nq][x] = fmaxf(mx[nq][x], fmaxf(s[kt][nq][x], s[kt][nq][x + 2]));
+          mx[nq][x] *= kFp8 || capped ? 1.f : rscale[nq][x];
+          passed |= mx[nq][x] > m[nq][x] + kLazy;
         }
       if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
+        for (int nq = 0; nq < kNQ; ++nq) {
           float alpha[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float fac = kFp8 || capped ? 1.f : rscale[mt][x];
-            float mx = -INFINITY;
+            float t = mx[nq][x];
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) mx = fmaxf(mx, fmaxf(s[mt][nt][2 * x], s[mt][nt][2 * x + 1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mn = fmaxf(m[mt][x], mx * fac);
-            alpha[x] = ex2_approx(m[mt][x] - (mn == -INFINITY ? 0.f : mn));
-            m[mt][x] = mn;
-            l[mt][x] *= alpha[x];
+            for (int sh = 4; sh < 32; sh <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, sh));
+            const float mn = fmaxf(m[nq][x], t);
+            alpha[x] = ex2_approx(m[nq][x] - (mn == -INFINITY ? 0.f : mn));
+            m[nq][x] = mn;
+            l[nq][x] *= alpha[x];
           }
 #pragma unroll
-          for (int j = 0; j < kDT; ++j) {
-            o[mt][j][0] *= alpha[0];
-            o[mt][j][1] *= alpha[0];
-            o[mt][j][2] *= alpha[1];
-            o[mt][j][3] *= alpha[1];
-          }
+          for (int j = 0; j < kDM; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nq][j][e] *= alpha[e & 1];
         }
       }
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
+      for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float fac = kFp8 || capped ? 1.f : rscale[mt][x];
-          const float shift = (m[mt][x] == -INFINITY ? 0.f : m[mt][x]) - (kFp8 ? kWeightShift : 0.f);
+          const float fac = kFp8 || capped ? 1.f : rscale[nq][x];
+          const float shift = (m[nq][x] == -INFINITY ? 0.f : m[nq][x]) - (kFp8 ? kWeightShift : 0.f);
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
+          for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float pr = ex2_approx(kFp8 ? s[mt][nt][2 * x + e] - shift : fmaf(s[mt][nt][2 * x + e], fac, -shift));
-              s[mt][nt][2 * x + e] = pr;
-              l[mt][x] = kFp8 ? fmaf(pr, inv_vs[kFp8 ? nt : 0][e], l[mt][x]) : l[mt][x] + pr;
+            for (int y = 0; y < 2; ++y) {
+              const float z = s[kt][nq][x + 2 * y];
+              const float pr = ex2_approx(kFp8 ? z - shift : fmaf(z, fac, -shift));
+              s[kt][nq][x + 2 * y] = pr;
+              l[nq][x] = kFp8 ? fmaf(pr, inv_vs[kFp8 ? kt : 0][y], l[nq][x]) : l[nq][x] + pr;
             }
         }
 
@@ -716,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             const int j = t0 + r;
             uint4* at = reinterpret_cast<uint4*>(st + G::kOpBytes + (lane / 8) * (kTok * 128) + swz<128>(r, lane % 8));
             bool odd = false;
-            if (lane < kChunks) {
+            if (lane < kRowChunks) {
               const uint4 v = *at;
               const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -724,77 +727,72 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             }
             if (!__any_sync(0xffffffffu, odd)) continue;
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
+            for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                uint32_t bits = 0;  // P[row][r], held by thread (r % 8) / 2 of the row's four (masks: no local array)
+                uint32_t bits = 0;  // P of key r and this lane's row, held by lane 4 (r % 8) + c (masks: no local array)
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) {
-                  const uint32_t here = nt == r / 8 ? 0xffffffffu : 0u, second = (r & 1) ? 0xffffffffu : 0u;
-                  bits |= here & ((second & __float_as_uint(s[mt][nt][2 * x + 1])) | (~second & __float_as_uint(s[mt][nt][2 * x])));
+                for (int kt = 0; kt < kKT; ++kt) {
+                  const uint32_t here = kt == r / 16 ? 0xffffffffu : 0u, second = (r & 8) ? 0xffffffffu : 0u;
+                  bits |= here & ((second & __float_as_uint(s[kt][nq][x + 2])) | (~second & __float_as_uint(s[kt][nq][x])));
                 }
-                const float pr = __uint_as_float(__shfl_sync(0xffffffffu, bits, (lane & ~3) | ((r & 7) >> 1)));
-                if (j < row_hi[mt][x] && j >= row_lo[mt][x]) {
+                const float pr = __uint_as_float(__shfl_sync(0xffffffffu, bits, 4 * (r & 7) + c));
+                if (j < row_hi[nq][x] && j >= row_lo[nq][x]) {
 #pragma unroll
-                  for (int dt = 0; dt < kDT; ++dt) {
-                    const float2 v = unpack_bf16(*reinterpret_cast<const uint32_t*>(
-                        st + G::kOpBytes + (dt / 8) * (kTok * 128) + swz<128>(r, dt % 8) + 4 * c));
-                    o[mt][dt][2 * x] = fmaf(pr, v.x, o[mt][dt][2 * x]);
-                    o[mt][dt][2 * x + 1] = fmaf(pr, v.y, o[mt][dt][2 * x + 1]);
-                  }
+                  for (int jj = 0; jj < kDM; ++jj)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {  // channel 16 jj + 8 y + g
+                      const int chunk = 2 * jj + y;
+                      const uint16_t v = *reinterpret_cast<const uint16_t*>(st + G::kOpBytes + (chunk / 8) * (kTok * 128) + swz<128>(r, chunk % 8) + 2 * g);
+                      o[nq][jj][x + 2 * y] = fmaf(pr, __uint_as_float((uint32_t)v << 16), o[nq][jj][x + 2 * y]);
+                    }
                 }
               }
             __syncwarp();
-            if (lane < kChunks) *at = make_uint4(0, 0, 0, 0);
+            if (lane < kRowChunks) *at = make_uint4(0, 0, 0, 0);
           }
         }
         __syncwarp();
       }
 
-      // ---- O += P V
-      if (!kFp8) {
-        const uint32_t vrow = lane & 15, vchunk = lane >> 4;
+      // ---- O^T += V^T P^T
 #pragma unroll
-        for (int kt = 0; kt < kTok / 16; ++kt) {
-          uint32_t hi[kMT][4], lo2[kMT][4];
+      for (int kt = 0; kt < kKT; ++kt) {
+        uint32_t ph[kNQ][2], pl[kNQ][2];
 #pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
+        for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              split2(s[mt][2 * kt + (x >> 1)][2 * (x & 1)], s[mt][2 * kt + (x >> 1)][2 * (x & 1) + 1], hi[mt][x], lo2[mt][x]);
-          // (four loads, then their products, hi before lo: a sum is met again after eight others)
-#pragma unroll
-          for (int d8 = 0; d8 < kDT / 8; ++d8) {
-            uint32_t vb[4][4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int d2 = 4 * d8 + q;
-              ldsm4t(vb[q], vs_addr + (d2 >> 2) * (kTok * 128) + swz<128>(kt * 16 + vrow, (d2 & 3) * 2 + vchunk));
+          for (int y = 0; y < 2; ++y) {
+            if (kFp8) {
+              ph[nq][y] = transpose8(pack_half(s[kt][nq][2 * y], s[kt][nq][2 * y + 1]));
+            } else {
+              uint32_t hi, lo2;
+              split2(s[kt][nq][2 * y], s[kt][nq][2 * y + 1], hi, lo2);
+              ph[nq][y] = transpose8(hi);
+              pl[nq][y] = transpose8(lo2);
             }
+          }
+        if (!kFp8) {
+          // (four loads, then their products, hi before lo: a sum is met again after the others)
+          const uint32_t vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = (lane >> 3) & 1;
+#pragma unroll
+          for (int j4 = 0; j4 < kDM / 4; ++j4) {
+            uint32_t va[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ldsm4t(va[q], vs_addr + j4 * (kTok * 128) + swz<128>(kt * 16 + vrow, 2 * q + vchunk));
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) {
-                  const uint32_t (&pa)[4] = part ? lo2[mt] : hi[mt];
-                  mma16816<false>(o[mt][8 * d8 + 2 * q], pa, vb[q][0], vb[q][1]);
-                  mma16816<false>(o[mt][8 * d8 + 2 * q + 1], pa, vb[q][2], vb[q][3]);
-                }
+                for (int nq = 0; nq < kNQ; ++nq)
+                  mma16816<false>(o[nq][4 * j4 + q], va[q], part ? pl[nq][0] : ph[nq][0], part ? pl[nq][1] : ph[nq][1]);
           }
-        }
-      } else {
-        // column g of product tile j stands for channel (kDP / 8) g + j: a thread's bytes of a row are contiguous
-        const uint8_t* vst = st + G::kOpBytes;
-#pragma unroll
-        for (int kt = 0; kt < kTok / 16; ++kt) {
-          uint32_t pa[kMT][4];
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              pa[mt][x] = pack_half(s[mt][2 * kt + (x >> 1)][2 * (x & 1)], s[mt][2 * kt + (x >> 1)][2 * (x & 1) + 1]);
-          constexpr int kWords = kDP / 32;  // 32-bit words of a row per thread: 4 or 2
+        } else {
+          // row g (g + 8) of product tile jj stands for channel (kDP / 8) g + 2 jj (and the next): a lane's
+          // bytes of a key are contiguous
+          const uint8_t* vst = st + G::kOpBytes;
+          constexpr int kWords = kDP / 32;  // 32-bit words of a key per lane: 4 or 2
           uint32_t vw[4][kWords];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -811,16 +809,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
           for (int x = 0; x < kWords; ++x)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const uint32_t e0 = __byte_perm(vw[0][x], vw[1][x], y ? 0x7362 : 0x5140);
-              const uint32_t e1 = __byte_perm(vw[2][x], vw[3][x], y ? 0x7362 : 0x5140);
-              uint32_t b00, b01, b10, b11;
-              e4m3x4_to_half2(e0, b00, b01);
-              e4m3x4_to_half2(e1, b10, b11);
+              uint32_t va[4];
+              e4m3x4_to_half2(__byte_perm(vw[0][x], vw[1][x], y ? 0x7362 : 0x5140), va[0], va[1]);
+              e4m3x4_to_half2(__byte_perm(vw[2][x], vw[3][x], y ? 0x7362 : 0x5140), va[2], va[3]);
 #pragma unroll
-              for (int mt = 0; mt < kMT; ++mt) {
-                mma16816<true>(o[mt][4 * x + 2 * y], pa[mt], b00, b10);
-                mma16816<true>(o[mt][4 * x + 2 * y + 1], pa[mt], b01, b11);
-              }
+              for (int nq = 0; nq < kNQ; ++nq) mma16816<true>(o[nq][2 * x + y], va, ph[nq][0], ph[nq][1]);
             }
         }
       }
@@ -833,39 +826,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     // before it left in shared memory, and the last one writes the result.  A warp that has passed its
     // sum on goes on with the next unit, whose tiles are under way already.  Barrier w passes the sum
     // from warp w - 1 to warp w; barrier kWarps gives its place back to warp 0.
-    // (a row's four threads hold parts of its sum l)
+    // (a row's eight lanes hold parts of its sum l)
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt)
+    for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 1);
-        l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 2);
-      }
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) l[nq][x] += __shfl_xor_sync(0xffffffffu, l[nq][x], sh);
     if (warp > 0) sm100::named_bar(warp, 64);
     else if (pieces > 0) sm100::named_bar(kWarps, 64);
     const bool mine_any = i_begin < i_end, sum_any = warp > 0 && s_any;
     if (sum_any) {
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) {
-        const float4 ml = s_ml[mt * 32];
+      for (int nq = 0; nq < kNQ; ++nq) {
+        const float4 ml = s_ml[nq * 32];
         float f[2], fs[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float mo = x ? ml.z : ml.x, lo2 = x ? ml.w : ml.y;
-          const float top = fmaxf(m[mt][x], mo);
+          const float top = fmaxf(m[nq][x], mo);
           // (a maximum of -inf: no key, or no number; what is added is then 0 or not a number)
-          f[x] = m[mt][x] == -INFINITY ? 1.f : ex2_approx(m[mt][x] - top);
+          f[x] = m[nq][x] == -INFINITY ? 1.f : ex2_approx(m[nq][x] - top);
           fs[x] = mo == -INFINITY ? 1.f : ex2_approx(mo - top);
-          m[mt][x] = top;
-          l[mt][x] = l[mt][x] * f[x] + lo2 * fs[x];
+          m[nq][x] = top;
+          l[nq][x] = l[nq][x] * f[x] + lo2 * fs[x];
         }
 #pragma unroll
-        for (int j = 0; j < kDT; ++j) {
-          const float4 t = s_sum[(mt * kDT + j) * 32];
-          o[mt][j][0] = o[mt][j][0] * f[0] + t.x * fs[0];
-          o[mt][j][1] = o[mt][j][1] * f[0] + t.y * fs[0];
-          o[mt][j][2] = o[mt][j][2] * f[1] + t.z * fs[1];
-          o[mt][j][3] = o[mt][j][3] * f[1] + t.w * fs[1];
+        for (int j = 0; j < kDM; ++j) {
+          const float4 t = s_sum[(nq * kDM + j) * 32];
+          const float tv[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nq][j][e] = o[nq][j][e] * f[e & 1] + tv[e] * fs[e & 1];
         }
       }
     }
@@ -873,10 +864,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     if (warp < kWarps - 1) {
       if (mine_any || warp == 0) {
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          s_ml[mt * 32] = make_float4(m[mt][0], l[mt][0], m[mt][1], l[mt][1]);
+        for (int nq = 0; nq < kNQ; ++nq) {
+          s_ml[nq * 32] = make_float4(m[nq][0], l[nq][0], m[nq][1], l[nq][1]);
 #pragma unroll
-          for (int j = 0; j < kDT; ++j) s_sum[(mt * kDT + j) * 32] = make_float4(o[mt][j][0], o[mt][j][1], o[mt][j][2], o[mt][j][3]);
+          for (int j = 0; j < kDM; ++j) s_sum[(nq * kDM + j) * 32] = make_float4(o[nq][j][0], o[nq][j][1], o[nq][j][2], o[nq][j][3]);
         }
         if (lane == 0) s_any = mine_any || sum_any;
       }
@@ -884,47 +875,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       sm100::named_bar_arrive(warp + 1, 64);
     } else {
       if (more) sm100::named_bar_arrive(kWarps, 64);
-      const bool whole = blk == 0 && take == n_blk;
       const int64_t slot = 2 * cta + (pieces == 0 ? 0 : 1);
+      if (blk == 0 && take == n_blk) {
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
+        for (int nq = 0; nq < kNQ; ++nq) {
+          const int row = row_base + 8 * nq + g, t = row / p.group;
+          __nv_bfloat16* row_out = nullptr;
+          if (row < p.rows) row_out = a.out + (((int64_t)b * a.new_tokens + t) * a.hq + h * p.group + row - t * p.group) * a.d;
+          float inv[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = mt * 16 + x * 8 + g, row = row_base + r;
-          if (row >= p.rows) continue;
-          const float top = m[mt][x], sum = l[mt][x];
-          const int t = row / p.group, head = h * p.group + row - t * p.group;
-          const int64_t at = ((int64_t)b * a.new_tokens + t) * a.hq + head;
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          // this thread's channels: pairs 8 j + 2 c (bf16), or kDT (2 c + y) + j (e4m3)
-          if (!kFp8) {
-#pragma unroll
-            for (int j = 0; j < kDT; ++j) {
-              const int ch = 8 * j + 2 * c;
-              if (ch >= a.d) continue;
-              if (whole) *reinterpret_cast<uint32_t*>(a.out + at * a.d + ch) = pack_bf16(o[mt][j][2 * x] * inv, o[mt][j][2 * x + 1] * inv);
-              else *reinterpret_cast<float2*>(p.part_o + (slot * kRows + r) * a.d + ch) = make_float2(o[mt][j][2 * x], o[mt][j][2 * x + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int j = 0; j < kDT; j += 4) {
-                const int ch = kDT * (2 * c + y) + j;
-                if (ch >= a.d) continue;
-                const float v[4] = {o[mt][j][2 * x + y], o[mt][j + 1][2 * x + y], o[mt][j + 2][2 * x + y], o[mt][j + 3][2 * x + y]};
-                if (whole)
-                  *reinterpret_cast<uint2*>(a.out + at * a.d + ch) = make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
-                else
-                  *reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * a.d + ch) = make_float4(v[0], v[1], v[2], v[3]);
-              }
+          for (int x = 0; x < 2; ++x) {
+            inv[x] = l[nq][x] == 0.f ? 0.f : 1.f / l[nq][x];
+            const int r = row_base + 8 * nq + 2 * c + x, rt = r / p.group;
+            if (g == 0 && r < p.rows && a.lse)
+              a.lse[((int64_t)b * a.new_tokens + rt) * a.hq + h * p.group + r - rt * p.group] = lse_of(m[nq][x], l[nq][x], kFp8 ? kWeightShift : 0.f);
           }
-          if (c == 0) {
-            if (!whole) p.part_ml[slot * kRows + r] = make_float2(top, sum);
-            else if (a.lse)
-              a.lse[at] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - (kFp8 ? kWeightShift : 0.f) + log2f(sum)) * 0.6931471805599453f;
-          }
+#pragma unroll
+          for (int j = 0; j < kDM; ++j) write_tile<kFp8, kDP>(o[nq][j], j, inv, row_out, a.d);
         }
+      } else {
+#pragma unroll
+        for (int nq = 0; nq < kNQ; ++nq) {
+          if (row_base + 8 * nq >= p.rows) continue;
+          p.part_ml[(slot * kNQ + nq) * 32 + lane] = make_float4(m[nq][0], l[nq][0], m[nq][1], l[nq][1]);
+#pragma unroll
+          for (int j = 0; j < kDM; ++j)
+            p.part_o[((slot * kNQ + nq) * kDM + j) * 32 + lane] = make_float4(o[nq][j][0], o[nq][j][1], o[nq][j][2], o[nq][j][3]);
+        }
+      }
       if (pieces == 0 && blk > 0 && blk + take == n_blk) {  // this CTA ends a unit that others began
         // the CTA of its first block; the unit is that CTA's first one if its share begins there, or in
         // the end (without blocks) of the unit before
@@ -941,21 +919,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 }
 
 // Joins the partial results of every unit that more than one CTA worked on, in the order of its
-// keys.  The launch's blocks take (unit, rows) jobs in turn: eight rows, a warp each, where a unit
-// has few partials; one row, its partials dealt to the eight warps, where it has many.
-constexpr int kJoinThreads = 256;
+// keys.  The launch's blocks take jobs in turn: a row tile, its channel tiles a warp each, where a unit
+// has few partials; a row tile's one channel tile, the partials dealt to the eight warps, where it
+// has many.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kFewPartials = 8;
 
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ DecodeParams p, int ctas, int rows_per_block,
-                                                                 float weight_shift) {
+template <bool kFp8, int kDP, int kNQ>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ DecodeParams p, int ctas) {
+  constexpr int kDM = kDP / 16;
   const AttnDecodeArgs& a = p.a;
   __shared__ int s_end[kMaxCtas];      // jobs up to and with CTA i's unit
   __shared__ int4 s_meta[kMaxCtas];
-  __shared__ int s_warp[kJoinThreads / 32];
-  __shared__ float s_o[kJoinThreads / 32][kAttnMaxDim];
-  __shared__ float2 s_ml[kJoinThreads / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ int s_warp[kJoinWarps];
+  __shared__ float4 s_o[kJoinWarps][32], s_ml[kJoinWarps][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   sm100::griddep_wait();
+  auto row_tiles = [&](int unit) {
+    const int rows = p.rows - (unit % p.row_blocks) * 8 * kNQ;
+    return min(kNQ, (rows + 7) / 8);
+  };
   int jobs[2] = {0, 0};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -963,11 +946,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     if (i < ctas) {
       const int4 mt = p.meta[i];
       s_meta[i] = mt;
-      if (mt.y > 0) {
-        const int rb = mt.z % p.row_blocks;
-        const int live = min(rows_per_block, p.rows - rb * rows_per_block);
-        jobs[k] = mt.y > kFewPartials ? live : (live + 7) / 8;
-      }
+      if (mt.y > 0) jobs[k] = row_tiles(mt.z) * (mt.y > kFewPartials ? kDM : 1);
     }
   }
   int incl = jobs[0] + jobs[1];
@@ -979,7 +958,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
   int before = 0, total = 0;
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
+  for (int w = 0; w < kJoinWarps; ++w) {
     if (w < warp) before += s_warp[w];
     total += s_warp[w];
   }
@@ -997,73 +976,80 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     }
     const int4 mt = s_meta[lo];
     const int local = job - (lo > 0 ? s_end[lo - 1] : 0);
-    const int rb = mt.z % p.row_blocks, bh = mt.z / p.row_blocks;
-    const int live = min(rows_per_block, p.rows - rb * rows_per_block);
     const bool many = mt.y > kFewPartials;
-    const int r = many ? local : local * 8 + warp;
+    const int nq = many ? local / kDM : local, jj = many ? local % kDM : warp;
     const int cta0 = mt.x >> 1;
-    auto slot = [&](int i) { return (int64_t)(i == 0 ? mt.x : 2 * (cta0 + i)) * rows_per_block + r; };
-    float top = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < live) {
-      const int step = many ? kJoinThreads / 32 : 1;
-      for (int i = many ? warp : 0; i < mt.y; i += step) top = fmaxf(top, p.part_ml[slot(i)].x);
-#pragma unroll 4
-      for (int i = many ? warp : 0; i < mt.y; i += step) {
-        const int64_t s = slot(i);
-        const float2 ml = p.part_ml[s];
-        const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - top);
-        sum = fmaf(ml.y, f, sum);
-        if (4 * lane < a.d) {
-          const float4 t = *reinterpret_cast<const float4*>(p.part_o + s * a.d + 4 * lane);
-          acc.x = fmaf(t.x, f, acc.x); acc.y = fmaf(t.y, f, acc.y);
-          acc.z = fmaf(t.z, f, acc.z); acc.w = fmaf(t.w, f, acc.w);
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? mt.x : 2 * (cta0 + i)) * kNQ + nq; };
+    // partials first, first + step, ..: their results relative to the largest reference met so far
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](const float4& ml, const float4& t) {
+      const float mo[2] = {ml.x, ml.z}, lo2[2] = {ml.y, ml.w}, tv[4] = {t.x, t.y, t.z, t.w};
+      float f[2], fs[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float top = fmaxf(m[x], mo[x]);
+        f[x] = m[x] == -INFINITY ? 1.f : ex2_approx(m[x] - top);
+        fs[x] = mo[x] == -INFINITY ? 1.f : ex2_approx(mo[x] - top);
+        m[x] = top;
+        l[x] = l[x] * f[x] + lo2[x] * fs[x];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = o[e] * f[e & 1] + tv[e] * fs[e & 1];
+    };
+    if (jj < kDM) {
+      constexpr int kBatch = 8;  // loads under way
+      const int step = many ? kJoinWarps : 1;
+      for (int i0 = many ? warp : 0; i0 < mt.y; i0 += kBatch * step) {
+        float4 ml[kBatch], t[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * step;
+          if (i < mt.y) {
+            const int64_t sl = slot(i);
+            ml[k] = p.part_ml[sl * 32 + lane];
+            t[k] = p.part_o[(sl * kDM + jj) * 32 + lane];
+          }
         }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (i0 + k * step < mt.y) add(ml[k], t[k]);
       }
     }
     if (many) {
       __syncthreads();
-      reinterpret_cast<float4*>(s_o[warp])[lane] = acc;
-      if (lane == 0) s_ml[warp] = make_float2(top, sum);
+      s_o[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
+      s_ml[warp][lane] = make_float4(m[0], l[0], m[1], l[1]);
       __syncthreads();
       if (warp != 0) continue;
-      top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, s_ml[w].x);
-      sum = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kJoinThreads / 32; ++w) {
-        const float f = s_ml[w].x == -INFINITY ? 1.f : ex2_approx(s_ml[w].x - top);
-        sum = fmaf(s_ml[w].y, f, sum);
-        const float4 t = reinterpret_cast<const float4*>(s_o[w])[lane];
-        acc.x = fmaf(t.x, f, acc.x); acc.y = fmaf(t.y, f, acc.y);
-        acc.z = fmaf(t.z, f, acc.z); acc.w = fmaf(t.w, f, acc.w);
-      }
+      for (int w = 1; w < kJoinWarps; ++w) add(s_ml[w][lane], s_o[w][lane]);
     }
-    if (r < live) {
-      const int row = rb * rows_per_block + r;
+    if (jj < kDM) {
+      const int bh = mt.z / p.row_blocks, row_base = (mt.z - bh * p.row_blocks) * 8 * kNQ + 8 * nq;
       const int b = bh / a.hkv, h = bh - b * a.hkv;
-      const int t = row / p.group, head = h * p.group + row - t * p.group;
-      const int64_t at = ((int64_t)b * a.new_tokens + t) * a.hq + head;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      if (4 * lane < a.d)
-        *reinterpret_cast<uint2*>(a.out + at * a.d + 4 * lane) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-      if (lane == 0 && a.lse)
-        a.lse[at] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - weight_shift + log2f(sum)) * 0.6931471805599453f;
+      auto row_at = [&](int row) {
+        const int t = row / p.group;
+        return ((int64_t)b * a.new_tokens + t) * a.hq + h * p.group + row - t * p.group;
+      };
+      float inv[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        inv[x] = l[x] == 0.f ? 0.f : 1.f / l[x];
+        const int r = row_base + 2 * c + x;
+        if (jj == 0 && g == 0 && r < p.rows && a.lse) a.lse[row_at(r)] = lse_of(m[x], l[x], kFp8 ? kWeightShift : 0.f);
+      }
+      write_tile<kFp8, kDP>(o, jj, inv, row_base + g < p.rows ? a.out + row_at(row_base + g) * a.d : nullptr, a.d);
     }
   }
 }
 
-size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+// Row tiles of one unit: as few as hold all rows of a (sequence, kv head), at most 4 (32 rows).
+int row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+int padded_dim(int d) { return d <= 64 ? 64 : 128; }
 
-// Rows of one row block: 16 while all rows of a (sequence, kv head) fit, else 32.
-int rows_per_block(int rows) { return rows <= 16 ? 16 : 32; }
-
-template <bool kFp8, int kDP, int kMT>
+template <bool kFp8, int kDP, int kNQ>
 cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
-  using G = Geo<kFp8, kDP, kMT>;
-  using SM = Smem<kFp8, kDP, kMT>;
+  using G = Geo<kFp8, kDP, kNQ>;
+  using SM = Smem<kFp8, kDP, kNQ>;
   static bool attr_done[64] = {};
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
@@ -1075,18 +1061,18 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   const int64_t units = (int64_t)a.batch * a.hkv * p.row_blocks;
   const int64_t cap = (int64_t)a.max_pages << a.page_shift;
   const int64_t most_blocks = cap > G::kBlockTok ? (cap + G::kBlockTok - 1) / G::kBlockTok : 1;
-  int64_t grid = (int64_t)kCtasPerSm * sms;
+  int64_t grid = (int64_t)G::kCtasPerSm * sms;
   if (grid > kMaxCtas) grid = kMaxCtas;
-  if (units < grid && units * most_blocks < grid) grid = units * most_blocks;
+  if (units < grid && units * (most_blocks + kUnitCost) < grid) grid = units * (most_blocks + kUnitCost);
   uint8_t* ws = a.workspace;
   p.status = reinterpret_cast<uint32_t*>(ws);
   p.meta = reinterpret_cast<int4*>(ws + kWorkspaceHeader);
-  p.part_ml = reinterpret_cast<float2*>(ws + kWorkspaceHeader + up256(kMaxCtas * sizeof(int4)));
-  p.part_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.part_ml) + up256((size_t)2 * kMaxCtas * SM::kRows * sizeof(float2)));
-  constexpr uint32_t kSmem = SM::kTotal + 1024;
-  cudaError_t e = set_smem_once(attn_decode_kernel<kFp8, kDP, kMT>, kSmem, attr_done);
+  p.part_ml = reinterpret_cast<float4*>(ws + kWorkspaceHeader + kMaxCtas * sizeof(int4));
+  p.part_o = p.part_ml + 2 * kMaxCtas * kNQ * 32;
+  constexpr uint32_t kSmem = SM::kTotal + 128;
+  cudaError_t e = set_smem_once(attn_decode_kernel<kFp8, kDP, kNQ>, kSmem, attr_done);
   if (e != cudaSuccess) return e;
-  attn_decode_kernel<kFp8, kDP, kMT><<<(unsigned)grid, kThreads, kSmem, stream>>>(p);
+  attn_decode_kernel<kFp8, kDP, kNQ><<<(unsigned)grid, G::kThreads, kSmem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || most_blocks == 1) return e;  // (no unit has two blocks: nothing to join)
   cudaLaunchConfig_t cfg = {};
@@ -1098,21 +1084,23 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel, p, (int)grid, (int)SM::kRows, kFp8 ? kWeightShift : 0.f);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kFp8, kDP, kNQ>, p, (int)grid);
 }
 
 template <bool kFp8, int kDP>
 cudaError_t launch_rows(const AttnDecodeArgs& a, cudaStream_t stream) {
-  return rows_per_block(a.new_tokens * (a.hq / a.hkv)) == 16 ? launch_typed<kFp8, kDP, 1>(a, stream)
-                                                             : launch_typed<kFp8, kDP, 2>(a, stream);
+  switch (row_tiles(a.new_tokens * (a.hq / a.hkv))) {
+    case 1: return launch_typed<kFp8, kDP, 1>(a, stream);
+    case 2: return launch_typed<kFp8, kDP, 2>(a, stream);
+    default: return launch_typed<kFp8, kDP, 4>(a, stream);
+  }
 }
 
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int32_t rows, int32_t d) {
-  const size_t r = rows_per_block(rows);
-  return kWorkspaceHeader + up256(kMaxCtas * sizeof(int4)) + up256(2 * kMaxCtas * r * sizeof(float2)) +
-         up256(2 * kMaxCtas * r * (size_t)d * sizeof(float));
+  const size_t tiles = row_tiles(rows);
+  return kWorkspaceHeader + kMaxCtas * sizeof(int4) + 2 * kMaxCtas * tiles * 32 * sizeof(float4) * (1 + padded_dim(d) / 16);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream) {
