@@ -9,7 +9,7 @@
 // head, T new tokens), 4 G T flops per 2 x 2 bytes (bf16): HBM, until G T is near 64.  So the design
 // is a stream of cache tiles with little else:
 //   - Split: the (sequence, kv head, row block) units are laid end to end as blocks of one tile of keys
-//     per warp, and every CTA (two or three per SM) takes an equal share of all blocks, wherever it
+//     per warp, and every CTA (two per SM) takes an equal share of all blocks, wherever it
 //     begins and ends, so ragged lengths cost no balance.  A unit that several CTAs share leaves fp32
 //     partial results (o, m, l) in the workspace, joined in a fixed order by a second, dependent launch.
 //   - Each of a CTA's warps streams its own tiles (one per block) through its own ring of stages, with
@@ -37,7 +37,7 @@
 namespace kda {
 namespace {
 
-constexpr int kMaxCtas = 3 * 160;     // bound used for the workspace (148 SMs on a B200)
+constexpr int kMaxCtas = 2 * 160;     // bound used for the workspace (148 SMs on a B200)
 constexpr float kLazy = 8.0f;         // how far (base 2) a score passes a row's reference before it moves
 constexpr float kWeightShift = 7.0f;  // fp16 weights: up to 2^(kLazy + kWeightShift) = 2^15
 
@@ -46,7 +46,6 @@ struct DecodeParams {
   int32_t group, rows, row_blocks;  // rows = new_tokens * group, of one (sequence, kv head)
   float4* part_o;                   // [2 * CTAs][row tile][channel tile][lane]: as the product leaves it
   float4* part_ml;                  // [2 * CTAs][row tile][lane]: (m, l) of the lane's two rows
-  int4* meta;                       // [CTAs]: first partial, partials, unit, 0
   uint32_t* status;
 };
 
@@ -109,28 +108,31 @@ __device__ __forceinline__ float lg2_approx(float x) {
 
 // tanh to about 2 units in the last place: below 1 Lambert's continued fraction cut after its fifth
 // denominator, x (945 + 105 x^2 + x^4) / (945 + 420 x^2 + 15 x^4) (off by 6e-8 at 1), above by 1 - 2 / (e^2x + 1).
-__device__ __forceinline__ float tanh_fast(float x) {
+__device__ __forceinline__ float tanh_near(float x) {
   const float q = x * x;
-  const float near = x * fmaf(q, q + 105.f, 945.f) * rcp_approx(fmaf(q, fmaf(q, 15.f, 420.f), 945.f));
+  return x * fmaf(q, q + 105.f, 945.f) * rcp_approx(fmaf(q, fmaf(q, 15.f, 420.f), 945.f));
+}
+__device__ __forceinline__ float tanh_any(float x) {
   const float far = fmaf(-2.f, rcp_approx(ex2_approx(x * (2.f * kLog2e)) + 1.f), 1.f);
-  return q < 1.f ? near : far;
+  return fabsf(x) < 1.f ? tanh_near(x) : far;
 }
 
 // Tile geometry.  kDP: the head size padded to 64 or 128 channels (the padding is zero in q and in
 // the loaded rows); kNQ: tiles of 8 rows per unit; kTok: keys of one warp's tile, 8 KB of K and V
-// together (4 KB for 64 e4m3 channels); a block is one tile per warp.  Up to 8 rows the registers
-// (168 a thread) leave room for 12 warps per SM, else (255) for 8.
+// together (4 KB for 64 e4m3 channels); a block is one tile per warp.  Two CTAs per SM: of 6 warps and
+// two stages for an e4m3 cache and up to 8 rows, whose registers (168 a thread) allow it, else of 4;
+// the bf16 cache's memory holds a third stage there instead (82 us against 85 for 3 CTAs, 64 x 4K tokens).
 template <bool kFp8, int kDP, int kNQ>
 struct Geo {
   static constexpr int kWarps = kNQ == 1 && kFp8 ? 6 : 4;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCtasPerSm = kNQ == 1 && !kFp8 ? 3 : 2;
+  static constexpr int kCtasPerSm = 2;
   static constexpr int kTok = kFp8 ? 32 : (kDP == 128 ? 16 : 32);
   static constexpr int kRowBytes = kFp8 ? kDP : 128;               // bytes of a row in one column block
   static constexpr int kColBlocks = kFp8 ? 1 : kDP / 64;           // 128-byte column blocks (bf16)
   static constexpr int kOpBytes = kTok * kRowBytes * kColBlocks;   // K (or V) of one tile
   static constexpr int kStageBytes = 2 * kOpBytes;
-  static constexpr int kWarpBytes = 16384;
+  static constexpr int kWarpBytes = kNQ == 1 && !kFp8 ? 24576 : 16384;
   static constexpr int kStages = kWarpBytes / kStageBytes;
   static constexpr int kBlockTok = kTok * kWarps;
   static constexpr int kScaleBytes = kFp8 ? 3 * kTok * 4 : 0;      // k scales; v scales, then their logarithms; reciprocals
@@ -140,6 +142,11 @@ struct Geo {
 template <int kRowBytes>
 __device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t chunk) {
   return kRowBytes == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+}
+
+// a / b for 0 <= a, 0 < b: by 32 bits where they suffice.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Keys [lo, hi) that any row of a sequence sees.
@@ -179,7 +186,7 @@ struct Walk {
       key_range(a, b, lo, len, nullptr);
       n_blk = num_blocks<kBlockTok>(lo, len);
       const int n_cost = n_blk + kUnitCost;
-      u = (int)(off / n_cost);
+      u = (int)divide(off, n_cost);
       blk = (int)(off - (int64_t)u * n_cost);
       const int step = (int)min((int64_t)(n_cost - blk), left);  // of the unit's cost; its blocks come first
       take = min(n_blk - blk, step);
@@ -254,6 +261,9 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ>::kThreads, Geo<kFp8, kDP, 
   __shared__ int s_b;
   __shared__ int64_t s_off;
 
+  // (this launch may begin while the one before it drains, and the join while this one does: each
+  // waits here for all that ran before)
+  sm100::griddep_wait();
   sm100::griddep_launch_dependents();
 
   // ---- this CTA's share [w0, w1) of all blocks, and the sequence it begins in
@@ -281,11 +291,8 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ>::kThreads, Geo<kFp8, kDP, 
   }
   const int64_t ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
   const int64_t cta = blockIdx.x;
-  if (cta >= ctas) {
-    if (tid == 0) p.meta[cta] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  const int64_t w0 = cta * total / ctas, w1 = (cta + 1) * total / ctas;
+  if (cta >= ctas) return;
+  const int64_t w0 = divide(cta * total, ctas), w1 = divide((cta + 1) * total, ctas);
   if (mine > 0 && before <= w0 && w0 < before + mine) {
     int64_t at = before;
     for (int b = b_first; b < b_last; ++b) {
@@ -409,7 +416,6 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ>::kThreads, Geo<kFp8, kDP, 
   };
   advance();
 
-  int4 meta = make_int4(0, 0, 0, 0);
   int pieces = 0, slot_out = 0;
   bool more = out.next(a, units_per_seq);
   while (more) {
@@ -454,12 +460,14 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ>::kThreads, Geo<kFp8, kDP, 
           if (SM::kQRegs) return *reinterpret_cast<const uint32_t*>(q_rows + (8 * nq + g) * (kDP * 2) + (((ch / 8) ^ g) << 4) + (ch % 8) * 2);
           return src && ch < a.d ? __ldg(reinterpret_cast<const unsigned int*>(src + ch)) : 0u;
         };
+        // (rows beyond the unit's are zero: their scores would else move references and pass the cap)
+        const uint32_t keep = row_base + nq * 8 + g < p.rows ? q_keep : 0u, sign = keep & q_sign;
         uint32_t f[kKS][2];
         if (!kFp8) {
 #pragma unroll
           for (int ks = 0; ks < kKS; ++ks) {
-            f[ks][0] = (load4(16 * ks + 2 * c) & q_keep) ^ q_sign;
-            f[ks][1] = (load4(16 * ks + 8 + 2 * c) & q_keep) ^ q_sign;
+            f[ks][0] = (load4(16 * ks + 2 * c) & keep) ^ sign;
+            f[ks][1] = (load4(16 * ks + 8 + 2 * c) & keep) ^ sign;
           }
         } else {
           // channels 64 j + 16 c + 4 s + {0..3} are k-step 4 j + s of this lane (as the key bytes are read)
@@ -472,7 +480,7 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ>::kThreads, Geo<kFp8, kDP, 
             wv[j][4] = v1.x; wv[j][5] = v1.y; wv[j][6] = v1.z; wv[j][7] = v1.w;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              wv[j][i] = (wv[j][i] & q_keep) ^ q_sign;
+              wv[j][i] = (wv[j][i] & keep) ^ sign;
               const float2 t = unpack_bf16(wv[j][i]);
               big = fmaxf(big, fmaxf(fabsf(t.x), fabsf(t.y)));
             }
@@ -603,34 +611,54 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ>::kThreads, Geo<kFp8, kDP, 
 
       // ---- scores, masks, the value scales' logarithms.  S becomes z (times the row's factor where it
       // is not yet applied: bf16 without a cap).
-      float inv_vs[kFp8 ? kKT : 1][2];
-      const bool capped = a.softcap > 0.f;
+      float kf[kKT][2], lv[kKT][2], inv_vs[kFp8 ? kKT : 1][2];
 #pragma unroll
-      for (int kt = 0; kt < kKT; ++kt) {
-        float kf[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
-        if (kFp8) {
+      for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int key = kt * 16 + g + 8 * y;
-            kf[y] = sc[key];
-            lv[y] = sc[kTok + key];
-            inv_vs[kFp8 ? kt : 0][y] = sc[2 * kTok + key];
-          }
+        for (int y = 0; y < 2; ++y) {
+          const int key = kt * 16 + g + 8 * y;
+          kf[kt][y] = kFp8 ? sc[key] : 1.f;
+          lv[kt][y] = kFp8 ? sc[kTok + key] : 0.f;
+          if (kFp8) inv_vs[kFp8 ? kt : 0][y] = sc[2 * kTok + key];
         }
-        if (capped) {
+      const bool capped = a.softcap > 0.f;
+      if (capped) {
+        // in the cap's units; scores beyond it are rare: the shorter form of the tangent for all, unless
+        // there is one
+        const float cap2 = a.softcap * kLog2e;
+        float most = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
           for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float z = kFp8 ? s[kt][nq][e] * kf[e >> 1] : s[kt][nq][e];
-              s[kt][nq][e] = fmaf(a.softcap * kLog2e, tanh_fast(z * rscale[nq][e & 1]), lv[e >> 1]);
+              float& z = s[kt][nq][e];
+              z *= kFp8 ? kf[kt][e >> 1] * rscale[nq][e & 1] : rscale[nq][e & 1];
+              most = fmaxf(most, fabsf(z));
             }
-        } else if (kFp8) {
+        if (__any_sync(0xffffffffu, most >= 1.f)) {
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+            for (int nq = 0; nq < kNQ; ++nq)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[kt][nq][e] = fmaf(cap2, tanh_any(s[kt][nq][e]), lv[kt][e >> 1]);
+        } else {
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+            for (int nq = 0; nq < kNQ; ++nq)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[kt][nq][e] = fmaf(cap2, tanh_near(s[kt][nq][e]), lv[kt][e >> 1]);
+        }
+      } else if (kFp8) {
+#pragma unroll
+        for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
           for (int nq = 0; nq < kNQ; ++nq)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[kt][nq][e] = fmaf(s[kt][nq][e] * kf[e >> 1], rscale[nq][e & 1], lv[e >> 1]);
-        }
+            for (int e = 0; e < 4; ++e) s[kt][nq][e] = fmaf(s[kt][nq][e] * kf[kt][e >> 1], rscale[nq][e & 1], lv[kt][e >> 1]);
       }
       if (edge) {
 #pragma unroll
@@ -903,51 +931,97 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ>::kThreads, Geo<kFp8, kDP, 
             p.part_o[((slot * kNQ + nq) * kDM + j) * 32 + lane] = make_float4(o[nq][j][0], o[nq][j][1], o[nq][j][2], o[nq][j][3]);
         }
       }
-      if (pieces == 0 && blk > 0 && blk + take == n_blk) {  // this CTA ends a unit that others began
-        // the CTA of its first block; the unit is that CTA's first one if its share begins there, or in
-        // the end (without blocks) of the unit before
-        const int64_t start = w0 - blk;
-        const int64_t c0 = ((start + 1) * ctas - 1) / total;
-        const int64_t first = 2 * c0 + (start - c0 * total / ctas <= kUnitCost ? 0 : 1);
-        meta = make_int4((int)first, (int)(cta - c0 + 1), (int)((int64_t)b * units_per_seq + u), 0);
-      }
     }
     ++pieces;
     slot_out = slot_out == 2 ? 0 : slot_out + 1;
   }
-  if (warp == kWarps - 1 && lane == 0) p.meta[cta] = meta;
 }
 
 // Joins the partial results of every unit that more than one CTA worked on, in the order of its
-// keys.  The launch's blocks take jobs in turn: a row tile, its channel tiles a warp each, where a unit
+// keys; fp32 sums.  The launch's blocks take jobs in turn: a row tile, its channel tiles a warp each, where a unit
 // has few partials; a row tile's one channel tile, the partials dealt to the eight warps, where it
 // has many.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kFewPartials = 8;
 
 template <bool kFp8, int kDP, int kNQ>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ DecodeParams p, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid_constant__ DecodeParams p, int grid) {
+  using G = Geo<kFp8, kDP, kNQ>;
   constexpr int kDM = kDP / 16;
   const AttnDecodeArgs& a = p.a;
-  __shared__ int s_end[kMaxCtas];      // jobs up to and with CTA i's unit
-  __shared__ int4 s_meta[kMaxCtas];
+  __shared__ int s_end[kMaxCtas];      // jobs up to and with the unit that CTA i ends
+  __shared__ int4 s_meta[kMaxCtas];    // that unit: first partial, partials, unit
   __shared__ int s_warp[kJoinWarps];
+  __shared__ int64_t s_sum[kJoinThreads];
   __shared__ float4 s_o[kJoinWarps][32], s_ml[kJoinWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  sm100::griddep_wait();
-  auto row_tiles = [&](int unit) {
-    const int rows = p.rows - (unit % p.row_blocks) * 8 * kNQ;
-    return min(kNQ, (rows + 7) / 8);
+  sm100::griddep_launch_dependents();
+
+  // Who worked on what follows from the lengths, as in the main kernel (which has begun, so what wrote
+  // them is done): found before the wait for its results.
+  const int64_t units_per_seq = (int64_t)a.hkv * p.row_blocks;
+  const int per = (a.batch + kJoinThreads - 1) / kJoinThreads;
+  auto seq_cost = [&](int b, int& n_blk) {
+    int lo, hi;
+    key_range(a, b, lo, hi, nullptr);
+    n_blk = num_blocks<G::kBlockTok>(lo, hi);
+    return (n_blk + kUnitCost) * units_per_seq;
   };
+  int n_blk;
+  int64_t mine = 0;
+  for (int b = tid * per; b < min(a.batch, (tid + 1) * per); ++b) mine += seq_cost(b, n_blk);
+  int64_t incl64 = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, incl64, o);
+    if (lane >= o) incl64 += t;
+  }
+  __shared__ int64_t s_wsum[kJoinWarps];
+  if (lane == 31) s_wsum[warp] = incl64;
+  __syncthreads();
+  int64_t cost = 0;
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (w < warp) incl64 += s_wsum[w];
+    cost += s_wsum[w];
+  }
+  s_sum[tid] = incl64;  // the cost up to and with this thread's sequences
+  __syncthreads();
+  const int ctas = (int)min(cost, (int64_t)grid);
+  auto row_tiles = [&](int unit) { return min(kNQ, (p.rows - (unit % p.row_blocks) * 8 * kNQ + 7) / 8); };
   int jobs[2] = {0, 0};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int i = 2 * tid + k;
-    if (i < ctas) {
-      const int4 mt = p.meta[i];
-      s_meta[i] = mt;
-      if (mt.y > 0) jobs[k] = row_tiles(mt.z) * (mt.y > kFewPartials ? kDM : 1);
+    if (i >= ctas) continue;
+    // CTA i ends a unit that others began if its share begins inside that unit's blocks and goes on to
+    // their end
+    const int64_t w0 = divide(i * cost, ctas), w1 = divide((i + 1) * cost, ctas);
+    int lo = 0, hi = kJoinThreads - 1;  // the first thread whose sum is beyond w0
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_sum[mid] > w0) hi = mid;
+      else lo = mid + 1;
     }
+    int64_t at = lo > 0 ? s_sum[lo - 1] : 0;
+    int b = lo * per;
+    for (;; ++b) {
+      const int64_t n = seq_cost(b, n_blk);
+      if (w0 < at + n || b + 1 >= a.batch) break;
+      at += n;
+    }
+    const int n_cost = n_blk + kUnitCost;
+    const int u = (int)divide(w0 - at, n_cost), blk = (int)(w0 - at - (int64_t)u * n_cost);
+    int4 mt = make_int4(0, 0, 0, 0);
+    if (blk > 0 && blk < n_blk && w1 - w0 >= n_blk - blk) {
+      // the CTA of the unit's first block; the unit is that CTA's first one if its share begins there,
+      // or in the end (without blocks) of the unit before
+      const int64_t start = w0 - blk;
+      const int64_t c0 = divide((start + 1) * ctas - 1, cost);
+      mt = make_int4((int)(2 * c0 + (start - divide(c0 * cost, ctas) <= kUnitCost ? 0 : 1)), (int)(i - c0 + 1),
+                     (int)((int64_t)b * units_per_seq + u), 0);
+      jobs[k] = row_tiles(mt.z) * (mt.y > kFewPartials ? kDM : 1);
+    }
+    s_meta[i] = mt;
   }
   int incl = jobs[0] + jobs[1];
 #pragma unroll
@@ -966,6 +1040,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   if (2 * tid < ctas) s_end[2 * tid] = end0;
   if (2 * tid + 1 < ctas) s_end[2 * tid + 1] = end1;
   __syncthreads();
+  sm100::griddep_wait();
 
   for (int job = blockIdx.x; job < total; job += gridDim.x) {
     int lo = 0, hi = ctas - 1;  // the first CTA whose end is beyond the job
@@ -997,7 +1072,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
       for (int e = 0; e < 4; ++e) o[e] = o[e] * f[e & 1] + tv[e] * fs[e & 1];
     };
     if (jj < kDM) {
-      constexpr int kBatch = 8;  // loads under way
+      constexpr int kBatch = 4;  // loads under way
       const int step = many ? kJoinWarps : 1;
       for (int i0 = many ? warp : 0; i0 < mt.y; i0 += kBatch * step) {
         float4 ml[kBatch], t[kBatch];
@@ -1066,24 +1141,26 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   if (units < grid && units * (most_blocks + kUnitCost) < grid) grid = units * (most_blocks + kUnitCost);
   uint8_t* ws = a.workspace;
   p.status = reinterpret_cast<uint32_t*>(ws);
-  p.meta = reinterpret_cast<int4*>(ws + kWorkspaceHeader);
-  p.part_ml = reinterpret_cast<float4*>(ws + kWorkspaceHeader + kMaxCtas * sizeof(int4));
+  p.part_ml = reinterpret_cast<float4*>(ws + kWorkspaceHeader);
   p.part_o = p.part_ml + 2 * kMaxCtas * kNQ * 32;
   constexpr uint32_t kSmem = SM::kTotal + 128;
   cudaError_t e = set_smem_once(attn_decode_kernel<kFp8, kDP, kNQ>, kSmem, attr_done);
   if (e != cudaSuccess) return e;
-  attn_decode_kernel<kFp8, kDP, kNQ><<<(unsigned)grid, G::kThreads, kSmem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || most_blocks == 1) return e;  // (no unit has two blocks: nothing to join)
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * sms));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(G::kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<kFp8, kDP, kNQ>, p);
+  if (e != cudaSuccess || most_blocks == 1) return e;  // (no unit has two blocks: nothing to join)
+  cfg.gridDim = dim3((unsigned)(2 * sms));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<kFp8, kDP, kNQ>, p, (int)grid);
 }
 
@@ -1100,7 +1177,7 @@ cudaError_t launch_rows(const AttnDecodeArgs& a, cudaStream_t stream) {
 
 size_t attn_decode_workspace_bytes(int32_t rows, int32_t d) {
   const size_t tiles = row_tiles(rows);
-  return kWorkspaceHeader + kMaxCtas * sizeof(int4) + 2 * kMaxCtas * tiles * 32 * sizeof(float4) * (1 + padded_dim(d) / 16);
+  return kWorkspaceHeader + 2 * kMaxCtas * tiles * 32 * sizeof(float4) * (1 + padded_dim(d) / 16);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream) {
