@@ -37,7 +37,10 @@
 namespace kda {
 namespace {
 
-constexpr int kMaxCtas = 2 * 160;     // bound used for the workspace (148 SMs on a B200)
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = kCtasPerSm * 160;  // bound used for the workspace (148 SMs on a B200)
 constexpr float kLazy = 8.0f;         // how far (base 2) a score passes a row's reference before it moves
 constexpr float kWeightShift = 7.0f;  // fp16 weights: up to 2^(kLazy + kWeightShift) = 2^15
 
@@ -119,14 +122,11 @@ __device__ __forceinline__ float tanh_any(float x) {
 
 // Tile geometry.  kDP: the head size padded to 64 or 128 channels (the padding is zero in q and in
 // the loaded rows); kNQ: tiles of 8 rows per unit; kTok: keys of one warp's tile, 8 KB of K and V
-// together (4 KB for 64 e4m3 channels); a block is one tile per warp.  Two CTAs per SM: of 6 warps and
-// two stages for an e4m3 cache and up to 8 rows, whose registers (168 a thread) allow it, else of 4;
-// the bf16 cache's memory holds a third stage there instead (82 us against 85 for 3 CTAs, 64 x 4K tokens).
+// together (4 KB for 64 e4m3 channels); a block is one tile per warp.  Two CTAs of 4 warps per SM:
+// their registers allow no more beyond 8 rows; up to 8, more warps (two CTAs of 6, three of 4) were no
+// faster for long sequences and slower for short ones.  The bf16 cache has room for a third stage there.
 template <bool kFp8, int kDP, int kNQ>
 struct Geo {
-  static constexpr int kWarps = kNQ == 1 && kFp8 ? 6 : 4;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCtasPerSm = 2;
   static constexpr int kTok = kFp8 ? 32 : (kDP == 128 ? 16 : 32);
   static constexpr int kRowBytes = kFp8 ? kDP : 128;               // bytes of a row in one column block
   static constexpr int kColBlocks = kFp8 ? 1 : kDP / 64;           // 128-byte column blocks (bf16)
@@ -216,12 +216,12 @@ struct Smem {
   static constexpr bool kQRegs = kNQ <= 2;                                            // query fragments in registers
   static constexpr int kQFragBytes = kQRegs ? 0 : kNQ * (kDP / 16) * 32 * 8;          // else here: one unit's
   static constexpr int kQRowBytes = kQRegs ? kRows * kDP * 2 : 0;                     // one unit's queries as they are
-  static constexpr int kScaleOff = G::kWarps * G::kWarpBytes;                         // (the rings come first)
-  static constexpr int kQOff = kScaleOff + G::kWarps * G::kStages * G::kScaleBytes;
+  static constexpr int kScaleOff = kWarps * G::kWarpBytes;                         // (the rings come first)
+  static constexpr int kQOff = kScaleOff + kWarps * G::kStages * G::kScaleBytes;
   static constexpr int kSumOff = kQOff + 2 * kQFragBytes + 3 * kQRowBytes;            // the warps' sum,
   static constexpr int kMlOff = kSumOff + kNQ * kDM * 32 * 16;                        // and each row's maximum and sum
   static constexpr int kScanOff = kMlOff + kNQ * 32 * 16;                             // one int64 per warp
-  static constexpr int kTotal = kScanOff + 8 * G::kWarps;
+  static constexpr int kTotal = kScanOff + 8 * kWarps;
 };
 
 // Rows of one row tile (o / l) to the output: o[jj] as the product leaves it, channel tile jj, the
@@ -242,11 +242,9 @@ __device__ __forceinline__ float lse_of(float m, float l, float shift) {
 }
 
 template <bool kFp8, int kDP, int kNQ>
-__global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ>::kThreads, Geo<kFp8, kDP, kNQ>::kCtasPerSm)
-    attn_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
   using G = Geo<kFp8, kDP, kNQ>;
   using SM = Smem<kFp8, kDP, kNQ>;
-  constexpr int kWarps = G::kWarps, kThreads = G::kThreads;
   constexpr int kTok = G::kTok, kKT = kTok / 16, kKS = kDP / 16, kDM = SM::kDM, kRows = SM::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128 - (sm100::smem_u32(smem_raw) & 127)) & 127);
@@ -395,11 +393,17 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ>::kThreads, Geo<kFp8, kDP, 
         const int64_t line = (((int64_t)in_h << a.page_shift) + (t0 & page_mask) + ld_row) * row_bytes;
         const uint8_t* ks = k_base + page * k_step + line;
         const uint8_t* vs = v_base + page * v_step + line;
+        constexpr int kFullPass = kPass * kDP * (kFp8 ? 1 : 2);
+        if (kPass * row_bytes == kFullPass) {  // (the steps as constants)
 #pragma unroll
-        for (int i = 0; i < kTok / kPass; ++i) {
-          copy_rows(i, ks, vs);
-          ks += kPass * row_bytes;
-          vs += kPass * row_bytes;
+          for (int i = 0; i < kTok / kPass; ++i) copy_rows(i, ks + i * kFullPass, vs + i * kFullPass);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTok / kPass; ++i) {
+            copy_rows(i, ks, vs);
+            ks += kPass * row_bytes;
+            vs += kPass * row_bytes;
+          }
         }
       } else {
 #pragma unroll 2
@@ -1144,7 +1148,7 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   const int64_t units = (int64_t)a.batch * a.hkv * p.row_blocks;
   const int64_t cap = (int64_t)a.max_pages << a.page_shift;
   const int64_t most_blocks = cap > G::kBlockTok ? (cap + G::kBlockTok - 1) / G::kBlockTok : 1;
-  int64_t grid = (int64_t)G::kCtasPerSm * sms;
+  int64_t grid = (int64_t)kCtasPerSm * sms;
   if (grid > kMaxCtas) grid = kMaxCtas;
   if (units < grid && units * (most_blocks + kUnitCost) < grid) grid = units * (most_blocks + kUnitCost);
   uint8_t* ws = a.workspace;
@@ -1159,7 +1163,7 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(G::kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = at;
