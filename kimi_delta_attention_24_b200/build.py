@@ -1,4 +1,5 @@
-"""Builds libkda_b200.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Builds libkda_b200.so (the C-ABI library) in-tree with nvcc for sm_100a, and attn_binding.so, the
+Python binding of its softmax-attention operators, with g++ against torch's headers.
 
     python -m kimi_delta_attention_24_b200.build [--force]
 """
@@ -21,6 +22,8 @@ LIB_PATH = os.path.join(LIB_DIR, "libkda_b200.so")
 SOURCES = ["kda_api.cu", "kda_recurrent.cu", "kda_chunked.cu", "kda_split.cu", "kda_fwd_static.cu",
            "kda_selftest.cu", "kda_decode.cu", "kda_kcp.cu", "kda_bwd.cu", "kda_pad.cu",
            "attn_api.cu", "attn_cache.cu", "attn_decode.cu"]
+BINDING_SRC = os.path.join(CSRC, "attn_binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "attn_binding.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH_FLAGS + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                            f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -44,6 +47,21 @@ def _stale(target: str, inputs) -> bool:
     return any(os.path.getmtime(i) > t for i in inputs)
 
 
+def _binding_command(out: str) -> list:
+    """g++ for the binding: torch's headers and libraries, found without importing torch."""
+    import importlib.util
+    import sysconfig
+
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda_home = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda_home, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(torch_dir, "lib")
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-I{INCLUDE}"] + [x for p in inc for x in ("-isystem", p)]
+            + [BINDING_SRC, "-o", out, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+               "-ltorch_cuda", "-ltorch_python"])
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
@@ -61,12 +79,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"the compiler failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr)
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def bind():
+        if force or _stale(BINDING_PATH, [BINDING_SRC, __file__] + deps):
+            tmp = BINDING_PATH + f".tmp{os.getpid()}"
+            run(_binding_command(tmp))
+            os.replace(tmp, BINDING_PATH)
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(bind)
         list(ex.map(run, jobs))
+        binding.result()
     if force or jobs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         run([nvcc] + ARCH_FLAGS + ["-shared", "-o", tmp] + objs)
