@@ -84,7 +84,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr)
 
     def bind():
-        if force or _stale(BINDING_PATH, [BINDING_SRC, __file__] + deps):
+        if force or _stale(BINDING_PATH, [BINDING_SRC, __file__, os.path.join(INCLUDE, "kda.h")]):
             tmp = BINDING_PATH + f".tmp{os.getpid()}"
             run(_binding_command(tmp))
             os.replace(tmp, BINDING_PATH)

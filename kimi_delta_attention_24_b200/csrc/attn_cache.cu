@@ -223,6 +223,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
   int head0 = (part - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * rows;
   const bool lane_on = live && 8 * sub < a.d;
 
+  // (the indexes first: loads come back in order, and the angles wait for the position)
+  const int slot_raw = kAppend && live ? __ldg(a.slots + token) : 0;
+  const int pos = live && a.cos_sin ? __ldg(a.positions + token) : 0;
   const __nv_bfloat16* src = in.x + token * in.stride + 8 * sub;
   RowVec raw[kRows];
 #pragma unroll
@@ -231,9 +234,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
   int turns = live ? min(batches, (in.heads - head0 + kRows - 1) / kRows) : 0;
   turns = max(turns, __shfl_xor_sync(0xffffffffu, turns, 16));
   if (kLanes == 8) turns = max(turns, __shfl_xor_sync(0xffffffffu, turns, 8));
-  int slot = 0;
+  int slot = slot_raw;
   if (kAppend && live) {
-    slot = __ldg(a.slots + token);
     if (slot >= a.num_slots) {
       if (a.status) atomicOr(a.status, kStatusBadIndex);
       slot = -1;
@@ -242,7 +244,6 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
   }
   const float* angles_row = nullptr;
   if (live && a.cos_sin) {
-    const int pos = __ldg(a.positions + token);
     if (pos < 0 || pos >= a.max_pos) {
       if (a.status) atomicOr(a.status, kStatusBadIndex);
       live = false;
@@ -325,128 +326,128 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
 constexpr int kBwdTurns = 8;
 
 template <int kLanes>
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, int most_turns) {
+__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, int most_turns, int q_blocks) {
   constexpr int kGroups = kThreads / kLanes;
   const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1), group = threadIdx.x / kLanes;
   const bool lane_on0 = 8 * sub < a.d;
   __shared__ __align__(16) float s_w[kGroups][kAttnMaxDim];
   sm100::griddep_launch_dependents();
-  for (int kind = 0; kind < 2; ++kind) {
-    const HeadRows& in = kind ? a.k : a.q;
-    const __nv_bfloat16* dy = kind ? a.dyk : a.dyq;
-    __nv_bfloat16* dx = kind ? a.dk : a.dq;
-    const int turns = min(most_turns, (in.heads + 1) / 2);
-    const int parts = (in.heads + 2 * turns - 1) / (2 * max(turns, 1));
-    const int items = (int)(a.tokens * parts);  // (below 2^31: checked by the host)
-    const bool norm = in.w != nullptr;
-    const float inv_d = 1.f / (float)a.d;
-    F2 w[4], dw[4];
-    {
-      float w8[8];
-      load8(in.w + 8 * sub, w8, norm && lane_on0, 1.f);
+  const bool kind = blockIdx.x >= q_blocks;  // queries, or keys
+  const uint32_t block = kind ? blockIdx.x - q_blocks : blockIdx.x, blocks = kind ? gridDim.x - q_blocks : q_blocks;
+  const HeadRows in = kind ? a.k : a.q;
+  const __nv_bfloat16* dy = kind ? a.dyk : a.dyq;
+  __nv_bfloat16* dx = kind ? a.dk : a.dq;
+  const int turns = min(most_turns, (in.heads + 1) / 2);
+  const int parts = (in.heads + 2 * turns - 1) / (2 * max(turns, 1));
+  const int items = (int)(a.tokens * parts);  // (below 2^31: checked by the host)
+  const bool norm = in.w != nullptr;
+  const float inv_d = 1.f / (float)a.d;
+  F2 w[4], dw[4];
+  {
+    float w8[8];
+    load8(in.w + 8 * sub, w8, norm && lane_on0, 1.f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[j] = f2(w8[2 * j], w8[2 * j + 1]);
-        dw[j] = f2(0.f, 0.f);
+    for (int j = 0; j < 4; ++j) {
+      w[j] = f2(w8[2 * j], w8[2 * j + 1]);
+      dw[j] = f2(0.f, 0.f);
+    }
+  }
+  // (all of a block's groups run the same number of turns: the shuffles are for whole warps)
+  for (uint32_t first = block * kGroups; first < (uint32_t)items; first += blocks * kGroups) {
+    const uint32_t item = first + group;
+    const int64_t token = item / (uint32_t)parts;
+    bool live = item < (uint32_t)items;
+    int head0 = (int)(item % (uint32_t)parts) * 2 * turns;
+    const __nv_bfloat16* x_row = in.x + token * in.stride + 8 * sub;
+    const __nv_bfloat16* dy_row = dy + token * in.heads * a.d + 8 * sub;
+    const bool in_range = live && lane_on0;
+    const int pos = live && a.cos_sin ? __ldg(a.positions + token) : 0;  // (before the rows: loads come back in order)
+    RowVec rx[2], rg[2];
+    auto load_two = [&](int head, bool on) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        rx[i] = load_row(x_row + (int64_t)(head + i) * a.d, on && in_range && head + i < in.heads);
+        rg[i] = load_row(dy_row + (int64_t)(head + i) * a.d, on && in_range && head + i < in.heads);
+      }
+    };
+    load_two(head0, true);
+    const float* row = nullptr;
+    if (live && a.cos_sin) {
+      if (pos < 0 || pos >= a.max_pos) {
+        if (a.status) atomicOr(a.status, kStatusBadIndex);
+        live = false;
+      } else {
+        row = a.cos_sin + (int64_t)pos * a.rot;
       }
     }
-    // (all of a block's groups run the same number of turns: the shuffles are for whole warps)
-    for (uint32_t first = blockIdx.x * kGroups; first < (uint32_t)items; first += gridDim.x * kGroups) {
-      const uint32_t item = first + group;
-      const int64_t token = item / (uint32_t)parts;
-      bool live = item < (uint32_t)items;
-      int head0 = (int)(item % (uint32_t)parts) * 2 * turns;
-      const __nv_bfloat16* x_row = in.x + token * in.stride + 8 * sub;
-      const __nv_bfloat16* dy_row = dy + token * in.heads * a.d + 8 * sub;
-      const bool in_range = live && lane_on0;
-      RowVec rx[2], rg[2];
-      auto load_two = [&](int head, bool on) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          rx[i] = load_row(x_row + (int64_t)(head + i) * a.d, on && in_range && head + i < in.heads);
-          rg[i] = load_row(dy_row + (int64_t)(head + i) * a.d, on && in_range && head + i < in.heads);
-        }
-      };
-      load_two(head0, true);
-      const float* row = nullptr;
-      if (live && a.cos_sin) {
-        const int pos = __ldg(a.positions + token);
-        if (pos < 0 || pos >= a.max_pos) {
-          if (a.status) atomicOr(a.status, kStatusBadIndex);
-          live = false;
-        } else {
-          row = a.cos_sin + (int64_t)pos * a.rot;
-        }
-      }
-      Angles ang;
-      load_angles<kLanes, true>(ang, row, a.rot, a.interleaved, nullptr, lane_on0);
+    Angles ang;
+    load_angles<kLanes, true>(ang, row, a.rot, a.interleaved, nullptr, lane_on0);
 #pragma unroll 1
-      for (int turn = 0; turn < turns; ++turn, head0 += 2) {
-        const RowVec cx[2] = {rx[0], rx[1]}, cg[2] = {rg[0], rg[1]};
-        load_two(head0 + 2, turn + 1 < turns);
-        Row8 g[2];
-        float sums[4];  // of x^2 and of u x, both rows
+    for (int turn = 0; turn < turns; ++turn, head0 += 2) {
+      const RowVec cx[2] = {rx[0], rx[1]}, cg[2] = {rg[0], rg[1]};
+      load_two(head0 + 2, turn + 1 < turns);
+      Row8 g[2];
+      float sums[4];  // of x^2 and of u x, both rows
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          g[i] = rotated(to_float(cg[i]), paired(cg[i], ang, a.interleaved), ang);
+      for (int i = 0; i < 2; ++i) {
+        g[i] = rotated(to_float(cg[i]), paired(cg[i], ang, a.interleaved), ang);
+        const Row8 x = to_float(cx[i]);
+        F2 ss = f2(0.f, 0.f), ux = f2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ss = fma2(x.v[j], x.v[j], ss);
+          ux = fma2(mul2(g[i].v[j], w[j]), x.v[j], ux);
+        }
+        const float2 s2 = un2(ss), u2 = un2(ux);
+        sums[i] = s2.x + s2.y;
+        sums[2 + i] = u2.x + u2.y;
+      }
+      const float total = sum4<kLanes>(sums);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float ss = __shfl_sync(0xffffffffu, total, sum4_lane<kLanes>(i));
+        const float ux = __shfl_sync(0xffffffffu, total, sum4_lane<kLanes>(2 + i));
+        Row8 out = g[i];
+        if (norm) {
+          const float r = rsqrtf(ss * inv_d + a.eps);
+          const float k = -(ux * inv_d * r * r * r);
+          const F2 r2 = f2(r, r), k2 = f2(k, k);
           const Row8 x = to_float(cx[i]);
-          F2 ss = f2(0.f, 0.f), ux = f2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            ss = fma2(x.v[j], x.v[j], ss);
-            ux = fma2(mul2(g[i].v[j], w[j]), x.v[j], ux);
+            if (live) dw[j] = fma2(mul2(g[i].v[j], r2), x.v[j], dw[j]);  // (a skipped token adds nothing)
+            out.v[j] = fma2(x.v[j], k2, mul2(mul2(g[i].v[j], w[j]), r2));
           }
-          const float2 s2 = un2(ss), u2 = un2(ux);
-          sums[i] = s2.x + s2.y;
-          sums[2 + i] = u2.x + u2.y;
         }
-        const float total = sum4<kLanes>(sums);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float ss = __shfl_sync(0xffffffffu, total, sum4_lane<kLanes>(i));
-          const float ux = __shfl_sync(0xffffffffu, total, sum4_lane<kLanes>(2 + i));
-          Row8 out = g[i];
-          if (norm) {
-            const float r = rsqrtf(ss * inv_d + a.eps);
-            const float k = -(ux * inv_d * r * r * r);
-            const F2 r2 = f2(r, r), k2 = f2(k, k);
-            const Row8 x = to_float(cx[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (live) dw[j] = fma2(mul2(g[i].v[j], r2), x.v[j], dw[j]);  // (a skipped token adds nothing)
-              out.v[j] = fma2(x.v[j], k2, mul2(mul2(g[i].v[j], w[j]), r2));
-            }
-          }
-          if (live && lane_on0 && head0 + i < in.heads)
-            *reinterpret_cast<uint4*>(dx + (token * in.heads + head0 + i) * a.d + 8 * sub) = to_bf16(out);
-        }
+        if (live && lane_on0 && head0 + i < in.heads)
+          *reinterpret_cast<uint4*>(dx + (token * in.heads + head0 + i) * a.d + 8 * sub) = to_bf16(out);
       }
     }
-    if (!norm) continue;
-    __syncthreads();
-    if (lane_on0) {
+  }
+  if (!norm) return;
+  __syncthreads();
+  if (lane_on0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&s_w[group][8 * sub + 2 * j]) = un2(dw[j]);
-    }
-    __syncthreads();
-    for (int ch = threadIdx.x; ch < a.d; ch += kThreads) {
-      float t = 0.f;
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&s_w[group][8 * sub + 2 * j]) = un2(dw[j]);
+  }
+  __syncthreads();
+  for (int ch = threadIdx.x; ch < a.d; ch += kThreads) {
+    float t = 0.f;
 #pragma unroll
-      for (int gr = 0; gr < kGroups; ++gr) t += s_w[gr][ch];
-      a.partials[((int64_t)blockIdx.x * 2 + kind) * kAttnMaxDim + ch] = t;
-    }
+    for (int gr = 0; gr < kGroups; ++gr) t += s_w[gr][ch];
+    a.partials[(int64_t)blockIdx.x * kAttnMaxDim + ch] = t;
   }
 }
 
 // dw = sum over the blocks' partial sums: one block per projection, 8 slices of blocks per channel.
-__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* partials, int blocks, float* dwq, float* dwk, int d) {
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* partials, int q_blocks, int blocks, float* dwq, float* dwk, int d) {
   __shared__ float s[8][kAttnMaxDim];
   const int ch = threadIdx.x & 127, slice = threadIdx.x >> 7, kind = blockIdx.x;
   sm100::griddep_wait();
   float t = 0.f;
   if (ch < d) {
 #pragma unroll 8
-    for (int i = slice; i < blocks; i += 8) t += partials[((int64_t)i * 2 + kind) * kAttnMaxDim + ch];
+    for (int i = (kind ? q_blocks : 0) + slice; i < (kind ? blocks : q_blocks); i += 8) t += partials[(int64_t)i * kAttnMaxDim + ch];
   }
   s[slice][ch] = t;
   __syncthreads();
@@ -561,7 +562,7 @@ int64_t rope_items(int64_t tokens, int32_t hq, int32_t hk, int32_t hv, int batch
   return tokens * (n(hq) + n(hk) + n(hv));
 }
 
-size_t rope_bwd_workspace_bytes() { return kWorkspaceHeader + (size_t)kBwdMaxBlocks * 2 * kAttnMaxDim * sizeof(float); }
+size_t rope_bwd_workspace_bytes() { return kWorkspaceHeader + (size_t)kBwdMaxBlocks * kAttnMaxDim * sizeof(float); }
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
   return a.d <= 64 ? launch_rope<8>(a, false, stream) : launch_rope<16>(a, false, stream);
@@ -575,15 +576,23 @@ cudaError_t launch_qk_norm_rope_bwd(const RopeBwdArgs& a, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const int lanes = a.d <= 64 ? 8 : 16;
-  // two blocks per SM; fewer rows per group where there would be too few groups for them
-  const int heads = std::max(a.q.heads, a.k.heads);
-  auto blocks = [&](int turns) { return (a.tokens * ((heads + 2 * turns - 1) / (2 * turns)) * lanes + kThreads - 1) / kThreads; };
+  // Two blocks per SM, shared by queries and keys as their heads are; fewer rows per group where there
+  // would be too few groups for them.
+  auto blocks = [&](int heads, int turns) { return (a.tokens * ((heads + 2 * turns - 1) / (2 * turns)) * lanes + kThreads - 1) / kThreads; };
   int turns = 1;
-  while (turns < kBwdTurns && blocks(2 * turns) >= 4 * (int64_t)sms) turns *= 2;
-  const int64_t grid = std::min<int64_t>(blocks(turns), std::min(kBwdMaxBlocks, 2 * sms));
+  while (turns < kBwdTurns && blocks(a.q.heads, 2 * turns) + blocks(a.k.heads, 2 * turns) >= 4 * (int64_t)sms) turns *= 2;
+  int64_t q_blocks = blocks(a.q.heads, turns), k_blocks = blocks(a.k.heads, turns);
+  const int64_t most = std::min(kBwdMaxBlocks, 2 * sms);
+  if (q_blocks + k_blocks > most) {
+    const int64_t share = most * a.q.heads / (a.q.heads + a.k.heads);
+    q_blocks = std::min(q_blocks, std::max<int64_t>(share, q_blocks > 0));
+    k_blocks = std::min(k_blocks, most - q_blocks);
+    if (k_blocks == 0 && a.k.heads > 0) k_blocks = 1;
+  }
+  const int64_t grid = q_blocks + k_blocks;
   if (grid > 0) {
-    if (lanes == 8) norm_rope_bwd_kernel<8><<<(unsigned)grid, kThreads, 0, stream>>>(a, turns);
-    else norm_rope_bwd_kernel<16><<<(unsigned)grid, kThreads, 0, stream>>>(a, turns);
+    if (lanes == 8) norm_rope_bwd_kernel<8><<<(unsigned)grid, kThreads, 0, stream>>>(a, turns, (int)q_blocks);
+    else norm_rope_bwd_kernel<16><<<(unsigned)grid, kThreads, 0, stream>>>(a, turns, (int)q_blocks);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -597,7 +606,7 @@ cudaError_t launch_qk_norm_rope_bwd(const RopeBwdArgs& a, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = grid > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, (const float*)a.partials, (int)grid, a.dwq, a.dwk, a.d);
+  return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, (const float*)a.partials, (int)q_blocks, (int)grid, a.dwq, a.dwk, a.d);
 }
 
 cudaError_t launch_kv_read(const KvReadArgs& a, cudaStream_t stream) {

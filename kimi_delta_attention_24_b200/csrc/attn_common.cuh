@@ -57,7 +57,7 @@ struct RopeBwdArgs {
   int64_t tokens;
   int32_t d, rot, max_pos, interleaved;
   float eps;
-  float* partials;            // [CTAs][2][kAttnMaxDim]
+  float* partials;            // [CTAs][kAttnMaxDim]
   uint32_t* status;
 };
 
