@@ -52,9 +52,8 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-// Two bf16 as fp32, in order or exchanged.
+// Two bf16 as fp32.
 __device__ __forceinline__ F2 bf2(uint32_t u) { return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
-__device__ __forceinline__ F2 bf2_swapped(uint32_t u) { return f2(__uint_as_float(u & 0xffff0000u), __uint_as_float(u << 16)); }
 
 struct RowVec {
   uint32_t u[4];  // 8 bf16
@@ -120,7 +119,8 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
 struct Angles {
   F2 own[4], cross[4];
   int partner;    // lane of the warp
-  uint32_t mask;  // 0 where nothing is rotated: an infinity there must not meet the zero in `cross`
+  uint32_t up, high;  // 2^16 and the upper half's mask; 0 where nothing is rotated: an infinity there must
+                      // not meet the zero in `cross`
 };
 
 template <int kLanes, bool kBack>
@@ -128,7 +128,8 @@ __device__ __forceinline__ void load_angles(Angles& g, const float* row, int rot
   const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1);
   const bool on = row != nullptr && 8 * sub < rot;
   const bool second = on && !interleaved && 8 * sub >= rot / 2;
-  g.mask = on ? 0xffffffffu : 0u;
+  g.up = on ? 65536u : 0u;
+  g.high = on ? 0xffff0000u : 0u;
   g.partner = on && !interleaved ? (second ? lane - rot / 16 : lane + rot / 16) : lane;
   float c[8], s[8], w[8];
   load8(weight + 8 * sub, w, weight != nullptr && lane_on, 1.f);
@@ -169,12 +170,11 @@ __device__ __forceinline__ void load_angles(Angles& g, const float* row, int rot
 // The channels that a row's rotation pairs with this lane's.
 __device__ __forceinline__ Row8 paired(const RowVec& raw, const Angles& g, int interleaved) {
   Row8 o;
-  if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o.v[i] = bf2_swapped(raw.u[i] & g.mask);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o.v[i] = bf2(__shfl_sync(0xffffffffu, raw.u[i], g.partner) & g.mask);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = interleaved ? raw.u[i] : __shfl_sync(0xffffffffu, raw.u[i], g.partner);
+    const float first = __uint_as_float(u * g.up), second = __uint_as_float(u & g.high);
+    o.v[i] = interleaved ? f2(second, first) : f2(first, second);
   }
   return o;
 }
@@ -226,12 +226,19 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
   // (the indexes first: loads come back in order, and the angles wait for the position)
   const int slot_raw = kAppend && live ? __ldg(a.slots + token) : 0;
   const int pos = live && a.cos_sin ? __ldg(a.positions + token) : 0;
-  const __nv_bfloat16* src = in.x + token * in.stride + 8 * sub;
-  RowVec raw[kRows];
+  int left = live ? in.heads - head0 : 0;  // rows from here on
+  const int in_step = 2 * a.d;             // bytes between rows
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(in.x + token * in.stride + (int64_t)head0 * a.d + 8 * sub);
+  auto load_rows = [&](RowVec (&r)[kRows], int first) {
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) raw[i] = load_row(src + (int64_t)(head0 + i) * a.d, lane_on && head0 + i < in.heads);
+    for (int i = 0; i < kRows; ++i)
+      r[i] = load_row(reinterpret_cast<const __nv_bfloat16*>(src + (first + i) * in_step), lane_on && first + i < left);
+  };
+  RowVec raw[kRows], more[kRows];
+  load_rows(raw, 0);
   // (the turns of the warp's group with the most: every lane takes part in every exchange)
-  int turns = live ? min(batches, (in.heads - head0 + kRows - 1) / kRows) : 0;
+  left = min(left, rows);
+  int turns = (left + kRows - 1) / kRows;
   turns = max(turns, __shfl_xor_sync(0xffffffffu, turns, 16));
   if (kLanes == 8) turns = max(turns, __shfl_xor_sync(0xffffffffu, turns, 8));
   int slot = slot_raw;
@@ -254,16 +261,33 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
   const bool norm = in.w != nullptr;
   Angles ang;
   load_angles<kLanes, false>(ang, kind == 2 ? nullptr : angles_row, a.rot, a.interleaved, in.w, lane_on);
-#pragma unroll 1
-  for (int turn = 0; turn < turns; ++turn, head0 += kRows) {
-    RowVec next[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      next[i] = load_row(src + (int64_t)(head0 + kRows + i) * a.d, lane_on && turn + 1 < batches && head0 + kRows + i < in.heads);
+
+  // where the rows go, and the bytes between them
+  const bool to_cache = kAppend && kind != 0;
+  uint8_t* dst;
+  float* scale_at = nullptr;
+  int out_step = in_step;
+  if (!to_cache) {
+    __nv_bfloat16* out = kind == 0 ? a.q_out : a.k_out;
+    dst = reinterpret_cast<uint8_t*>(out + (token * in.heads + head0) * a.d + 8 * sub);
+  } else {
+    constexpr int kBytes = kQuant ? 1 : 2;
+    const int64_t page = slot >> a.page_shift;
+    const int64_t line = ((int64_t)head0 << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
+    const int64_t at = page * (kind == 1 ? a.k_page_stride : a.v_page_stride) + line * a.d + 8 * sub;
+    dst = static_cast<uint8_t*>(kind == 1 ? a.k_cache : a.v_cache) + at * kBytes;
+    out_step = (a.d * kBytes) << a.page_shift;
+    if (kQuant) scale_at = (kind == 1 ? a.k_scale : a.v_scale) + ((page * in.heads) << a.page_shift) + line;
+  }
+  const float inv_d = 1.f / (float)a.d;
+  const bool write = live && lane_on;
+
+  auto work = [&](const RowVec (&cur)[kRows], RowVec (&next)[kRows]) {
+    load_rows(next, kRows);
     float ss[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const Row8 x = to_float(raw[i]);
+      const Row8 x = to_float(cur[i]);
       F2 t = mul2(x.v[0], x.v[0]);
 #pragma unroll
       for (int j = 1; j < 4; ++j) t = fma2(x.v[j], x.v[j], t);
@@ -271,50 +295,45 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
       ss[i] = u.x + u.y;
     }
     const float total = sum4<kLanes>(ss);
-    const float rr = norm ? rsqrtf(total * (1.f / (float)a.d) + a.eps) : 1.f;
+    const float rr = norm ? rsqrtf(total * inv_d + a.eps) : 1.f;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const float r = __shfl_sync(0xffffffffu, rr, sum4_lane<kLanes>(i));
-      Row8 x = rotated(to_float(raw[i]), paired(raw[i], ang, a.interleaved), ang);
+      Row8 x = rotated(to_float(cur[i]), paired(cur[i], ang, a.interleaved), ang);
       const F2 r2 = f2(r, r);
 #pragma unroll
       for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], r2);
-      const int head = head0 + i;
-      const bool on = live && lane_on && head < in.heads;
-      if (!kAppend || kind == 0) {
-        __nv_bfloat16* out = kind == 0 ? a.q_out : a.k_out;
-        if (on) *reinterpret_cast<uint4*>(out + (token * in.heads + head) * a.d + 8 * sub) = to_bf16(x);
-      }
-      if (kAppend) {
-        const int64_t page = slot >> a.page_shift;
-        const int at = slot & ((1 << a.page_shift) - 1);
-        const int64_t row = ((int64_t)head << a.page_shift) + at;
-        const int64_t base = page * (kind == 1 ? a.k_page_stride : a.v_page_stride) + row * a.d + 8 * sub;
-        if (!kQuant) {
-          if (on && kind != 0) {
-            // (values as they are)
-            const uint4 v = kind == 2 ? make_uint4(raw[i].u[0], raw[i].u[1], raw[i].u[2], raw[i].u[3]) : to_bf16(x);
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(kind == 1 ? a.k_cache : a.v_cache) + base) = v;
-          }
-        } else {
-          // the largest magnitude by its bits: an infinity or NaN is larger than every number
-          uint32_t big = 0;
+      const bool on = write && i < left;
+      uint32_t big = 0;
+      if (kQuant) {
+        // the largest magnitude by its bits: an infinity or NaN is larger than every number
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 t = un2(x.v[j]);
-            big = max(big, max(__float_as_uint(t.x) & 0x7fffffffu, __float_as_uint(t.y) & 0x7fffffffu));
-          }
-          big = group_max<kLanes>(big);
-          if (on && kind != 0) {
-            const float scale = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : fmaxf(__fdiv_rn(__uint_as_float(big), kE4M3Max), kKvScaleFloor);
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(kind == 1 ? a.k_cache : a.v_cache) + base) = e4m3_codes(x, scale);
-            if (sub == 0) (kind == 1 ? a.k_scale : a.v_scale)[((page * in.heads) << a.page_shift) + row] = scale;
-          }
+        for (int j = 0; j < 4; ++j) {
+          const float2 t = un2(x.v[j]);
+          big = max(big, max(__float_as_uint(t.x) & 0x7fffffffu, __float_as_uint(t.y) & 0x7fffffffu));
         }
+        big = group_max<kLanes>(big);
+      }
+      if (!on) continue;
+      if (kQuant && to_cache) {
+        const float scale = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : fmaxf(__fdiv_rn(__uint_as_float(big), kE4M3Max), kKvScaleFloor);
+        *reinterpret_cast<uint2*>(dst + i * out_step) = e4m3_codes(x, scale);
+        if (sub == 0) scale_at[i << a.page_shift] = scale;
+      } else {
+        // (values go to a bf16 cache as they are)
+        *reinterpret_cast<uint4*>(dst + i * out_step) =
+            kAppend && !kQuant && kind == 2 ? make_uint4(cur[i].u[0], cur[i].u[1], cur[i].u[2], cur[i].u[3]) : to_bf16(x);
       }
     }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) raw[i] = next[i];
+    left -= kRows;
+    src += kRows * in_step;
+    dst += kRows * out_step;
+    if (kQuant) scale_at += (int64_t)kRows << a.page_shift;
+  };
+#pragma unroll 1
+  for (int turn = 0; turn < turns; turn += 2) {
+    work(raw, more);
+    if (turn + 1 < turns) work(more, raw);
   }
 }
 
