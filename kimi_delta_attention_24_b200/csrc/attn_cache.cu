@@ -634,7 +634,7 @@ cudaError_t launch_kv_read(const KvReadArgs& a, cudaStream_t stream) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   const int lanes = a.d <= 64 ? 8 : 16;
   const int64_t items = a.total * ((2 * a.heads + kReadRows - 1) / kReadRows);
-  const int64_t grid = std::min<int64_t>((items * lanes + kThreads - 1) / kThreads, 8 * sms);
+  const int64_t grid = std::min<int64_t>((items * lanes + kThreads - 1) / kThreads, 16 * sms);
   if (lanes == 8) {
     if (a.k_scale) kv_read_kernel<8, true><<<(unsigned)grid, kThreads, 0, stream>>>(a);
     else kv_read_kernel<8, false><<<(unsigned)grid, kThreads, 0, stream>>>(a);
