@@ -121,7 +121,7 @@ __device__ __forceinline__ float tanh_any(float x) {
 }
 
 // Tile geometry.  kDP: the head size padded to 64 or 128 channels (the padding is zero in q and in
-// the loaded rows); kNQ: tiles of 8 rows per unit; kTok: keys of one warp's tile, 8 KB of K and V
+// the loaded rows); kNQ: tiles of 8 rows per unit (1 or 2); kTok: keys of one warp's tile, 8 KB of K and V
 // together (4 KB for 64 e4m3 channels); a block is one tile per warp.  Two CTAs of 4 warps per SM:
 // their registers allow no more beyond 8 rows; up to 8, more warps (two CTAs of 6, three of 4) were no
 // faster for long sequences and slower for short ones.  The bf16 cache has room for a third stage there.
@@ -213,12 +213,10 @@ template <bool kFp8, int kDP, int kNQ>
 struct Smem {
   using G = Geo<kFp8, kDP, kNQ>;
   static constexpr int kRows = 8 * kNQ, kDM = kDP / 16;
-  static constexpr bool kQRegs = kNQ <= 2;                                            // query fragments in registers
-  static constexpr int kQFragBytes = kQRegs ? 0 : kNQ * (kDP / 16) * 32 * 8;          // else here: one unit's
-  static constexpr int kQRowBytes = kQRegs ? kRows * kDP * 2 : 0;                     // one unit's queries as they are
+  static constexpr int kQRowBytes = kRows * kDP * 2;                                  // one unit's queries as they are
   static constexpr int kScaleOff = kWarps * G::kWarpBytes;                         // (the rings come first)
   static constexpr int kQOff = kScaleOff + kWarps * G::kStages * G::kScaleBytes;
-  static constexpr int kSumOff = kQOff + 2 * kQFragBytes + 3 * kQRowBytes;            // the warps' sum,
+  static constexpr int kSumOff = kQOff + 3 * kQRowBytes;            // the warps' sum,
   static constexpr int kMlOff = kSumOff + kNQ * kDM * 32 * 16;                        // and each row's maximum and sum
   static constexpr int kScanOff = kMlOff + kNQ * 32 * 16;                             // one int64 per warp
   static constexpr int kTotal = kScanOff + 8 * kWarps;
@@ -367,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
       const int t0 = in_tok + in_i * G::kBlockTok;
       const uint32_t st = ring + stage_in * G::kStageBytes;
-      if (SM::kQRegs && in_first) {
+      if (in_first) {
         // the unit's queries come with its first tile: a load that is waited for at the unit's start
         // would queue behind all the copies under way.  All four warps copy them (the same bytes); of
         // three places the one behind a warp that lags and before one that leads is free.
@@ -439,8 +437,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 
     // ---- the rows' key ranges, their queries as fragments.  A lane works on the scores of rows
     // 2 c + {0, 1} of each row tile, and holds the queries of row g.
-    uint2* q_smem = reinterpret_cast<uint2*>(smem + SM::kQOff + (pieces & 1) * SM::kQFragBytes) + lane;
-    uint32_t qf[SM::kQRegs ? kNQ : 1][SM::kQRegs ? kKS : 1][2];
+    uint32_t qf[kNQ][kKS][2];
     float rscale[kNQ][2];   // score factor of the lane's rows
     int row_hi[kNQ][2], row_lo[kNQ][2];
 #pragma unroll
@@ -457,24 +454,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       const uint8_t* q_rows = smem + SM::kQOff + slot_out * SM::kQRowBytes;
 #pragma unroll
       for (int nq = 0; nq < kNQ; ++nq) {
-        const __nv_bfloat16* src = nullptr;
-        if (!SM::kQRegs) {
-          const int r = row_base + nq * 8 + g;
-          const int t = r / p.group, head = h * p.group + r - t * p.group;
-          if (r < p.rows) src = a.q + (((int64_t)b * a.new_tokens + t) * a.hq + head) * a.d;
-        }
-        // `ch` .. of row g, as they are in the ring or in global memory
-        auto load16 = [&](int ch) {
-          if (SM::kQRegs) return *reinterpret_cast<const uint4*>(q_rows + (8 * nq + g) * (kDP * 2) + (((ch / 8) ^ g) << 4));
-          return src && ch < a.d ? __ldg(reinterpret_cast<const uint4*>(src + ch)) : make_uint4(0, 0, 0, 0);
-        };
-        auto load4 = [&](int ch) {
-          if (SM::kQRegs) return *reinterpret_cast<const uint32_t*>(q_rows + (8 * nq + g) * (kDP * 2) + (((ch / 8) ^ g) << 4) + (ch % 8) * 2);
-          return src && ch < a.d ? __ldg(reinterpret_cast<const unsigned int*>(src + ch)) : 0u;
-        };
+        const uint8_t* q_row = q_rows + (8 * nq + g) * (kDP * 2);
+        auto load16 = [&](int ch) { return *reinterpret_cast<const uint4*>(q_row + (((ch / 8) ^ g) << 4)); };
+        auto load4 = [&](int ch) { return *reinterpret_cast<const uint32_t*>(q_row + (((ch / 8) ^ g) << 4) + (ch % 8) * 2); };
         // (rows beyond the unit's are zero: their scores would else move references and pass the cap)
         const uint32_t keep = row_base + nq * 8 + g < p.rows ? q_keep : 0u, sign = keep & q_sign;
-        uint32_t f[kKS][2];
+        uint32_t (&f)[kKS][2] = qf[nq];
         if (!kFp8) {
 #pragma unroll
           for (int ks = 0; ks < kKS; ++ks) {
@@ -513,24 +498,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
               f[4 * j + i / 2][i & 1] = pack_half(t.x * down, t.y * down);
             }
         }
-#pragma unroll
-        for (int ks = 0; ks < kKS; ++ks) {
-          if (SM::kQRegs) {
-            qf[SM::kQRegs ? nq : 0][SM::kQRegs ? ks : 0][0] = f[ks][0];
-            qf[SM::kQRegs ? nq : 0][SM::kQRegs ? ks : 0][1] = f[ks][1];
-          } else {
-            // all warps write the same; two units' queries alternate, and a warp is at most one unit
-            // ahead of another (the chain of sums below)
-            q_smem[(nq * kKS + ks) * 32] = make_uint2(f[ks][0], f[ks][1]);
-          }
-        }
       }
-      if (!SM::kQRegs) __syncwarp();
-    };
-    if (!SM::kQRegs) make_fragments();
-    auto query = [&](int nq, int ks) {
-      if (SM::kQRegs) return make_uint2(qf[SM::kQRegs ? nq : 0][SM::kQRegs ? ks : 0][0], qf[SM::kQRegs ? nq : 0][SM::kQRegs ? ks : 0][1]);
-      return q_smem[(nq * kKS + ks) * 32];
     };
 
     float o[kNQ][kDM][4];         // O^T: rows 2 c + (e & 1); channels 16 jj + g + 8 (e >> 1), or (kDP / 8) g + 2 jj + (e >> 1) (e4m3)
@@ -553,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       else if (ahead == 1) cp_async_wait<0>();
       else cp_async_wait<2>();
       __syncwarp();
-      if (SM::kQRegs && i == i_begin) make_fragments();
+      if (i == i_begin) make_fragments();
       uint8_t* st = stages + stage_out * G::kStageBytes;
       const uint32_t ks_addr = sm100::smem_u32(st), vs_addr = ks_addr + G::kOpBytes;
       float* sc = scales + stage_out * 3 * kTok;
@@ -583,8 +551,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             ldsm4(ka, ks_addr + (ks >> 2) * (kTok * 128) + swz<128>(kt * 16 + mrow, (ks & 3) * 2 + mchunk));
 #pragma unroll
             for (int nq = 0; nq < kNQ; ++nq) {
-              const uint2 q = query(nq, ks);
-              mma16816<false>(sp[ks % kParts][kt][nq], ka, q.x, q.y);
+              mma16816<false>(sp[ks % kParts][kt][nq], ka, qf[nq][ks][0], qf[nq][ks][1]);
             }
           }
       } else {
@@ -605,8 +572,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
               e4m3x4_to_half2(word(1), ka[1], ka[3]);
 #pragma unroll
               for (int nq = 0; nq < kNQ; ++nq) {
-                const uint2 q = query(nq, 4 * j + q4);
-                mma16816<true>(sp[q4 % kParts][kt][nq], ka, q.x, q.y);
+                mma16816<true>(sp[q4 % kParts][kt][nq], ka, qf[nq][4 * j + q4][0], qf[nq][4 * j + q4][1]);
               }
             }
         }
@@ -1129,8 +1095,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
   }
 }
 
-// Row tiles of one unit: as few as hold all rows of a (sequence, kv head), at most 4 (32 rows).
-int row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// Row tiles of one unit: 1 up to 8 rows of a (sequence, kv head), else 2, and as many units as the rows
+// need.  (Units of 4 tiles read a long cache once for 32 rows, but took as long per row there, and up to
+// 1.6 times as long for short sequences: 851 against 555 us for 80 rows of 208 x 402 tokens.)
+int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
 int padded_dim(int d) { return d <= 64 ? 64 : 128; }
 
 template <bool kFp8, int kDP, int kNQ>
@@ -1180,8 +1148,7 @@ template <bool kFp8, int kDP>
 cudaError_t launch_rows(const AttnDecodeArgs& a, cudaStream_t stream) {
   switch (row_tiles(a.new_tokens * (a.hq / a.hkv))) {
     case 1: return launch_typed<kFp8, kDP, 1>(a, stream);
-    case 2: return launch_typed<kFp8, kDP, 2>(a, stream);
-    default: return launch_typed<kFp8, kDP, 4>(a, stream);
+    default: return launch_typed<kFp8, kDP, 2>(a, stream);
   }
 }
 

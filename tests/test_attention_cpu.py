@@ -116,10 +116,10 @@ def test_decode_refusals(lib, kw, status):
 def test_workspace_sizes(lib):
     assert lib.kda_qk_norm_rope_bwd_workspace_size() >= 256 + 296 * 128 * 4  # a partial sum for each of two CTAs on 148 SMs
     size = kda.attn_decode_workspace_size
-    # two partial results of a unit's rows (at most 32 at a time) for each of at least two CTAs on each of 148 SMs
+    # two partial results of a unit's rows (at most 16 at a time) for each of at least two CTAs on each of 148 SMs
     assert size(1, 32, 8, 128) >= 256 + 2 * 296 * 4 * (128 + 2) * 4
     assert size(4, 32, 8, 128) >= 256 + 2 * 296 * 16 * (128 + 2) * 4
-    assert size(20, 32, 8, 64) >= 256 + 2 * 296 * 32 * (64 + 2) * 4
+    assert size(20, 32, 8, 64) >= 256 + 2 * 296 * 16 * (64 + 2) * 4
     assert size(1, 7, 2, 128) == size(0, 8, 8, 128) == size(1, 8, 8, 72) == 256
 
 
