@@ -17,7 +17,8 @@
 //     also across the ends of units; about 130 KB of copies in flight per SM.  (TMA boxes instead cost
 //     the issuing warp 800 to 900 cycles a tile, four boxes each, of 2600 to 3400.)
 //   - The warps' results of a unit meet as a chain through shared memory, so that no warp waits for a
-//     slower one before it goes on with the next unit.
+//     slower one before it goes on with the next unit.  With very many units (kSolo) each warp takes a
+//     share of its own instead.
 //   - The products are transposed, S^T = K Q^T and O^T = V^T P^T, mma.sync m16n8k16 with the keys (the
 //     channels) as the 16 and 8 rows of queries as the 8: a unit of up to 8 rows (one kv head's group
 //     at T = 1) wastes half as much of each instruction, and half the registers, as with 16 rows.
@@ -47,8 +48,8 @@ constexpr float kWeightShift = 7.0f;  // fp16 weights: up to 2^(kLazy + kWeightS
 struct DecodeParams {
   AttnDecodeArgs a;
   int32_t group, rows, row_blocks;  // rows = new_tokens * group, of one (sequence, kv head)
-  float4* part_o;                   // [2 * CTAs][row tile][channel tile][lane]: as the product leaves it
-  float4* part_ml;                  // [2 * CTAs][row tile][lane]: (m, l) of the lane's two rows
+  float4* part_o;                   // [2 * shares][row tile][channel tile][lane]: as the product leaves it
+  float4* part_ml;                  // [2 * shares][row tile][lane]: (m, l) of the lane's two rows
   uint32_t* status;
 };
 
@@ -125,7 +126,7 @@ __device__ __forceinline__ float tanh_any(float x) {
 // together (4 KB for 64 e4m3 channels); a block is one tile per warp.  Two CTAs of 4 warps per SM:
 // their registers allow no more beyond 8 rows; up to 8, more warps (two CTAs of 6, three of 4) were no
 // faster for long sequences and slower for short ones.  The bf16 cache has room for a third stage there.
-template <bool kFp8, int kDP, int kNQ>
+template <bool kFp8, int kDP, int kNQ, bool kSolo>
 struct Geo {
   static constexpr int kTok = kFp8 ? 32 : (kDP == 128 ? 16 : 32);
   static constexpr int kRowBytes = kFp8 ? kDP : 128;               // bytes of a row in one column block
@@ -134,7 +135,8 @@ struct Geo {
   static constexpr int kStageBytes = 2 * kOpBytes;
   static constexpr int kWarpBytes = kNQ == 1 && !kFp8 ? 24576 : 16384;
   static constexpr int kStages = kWarpBytes / kStageBytes;
-  static constexpr int kBlockTok = kTok * kWarps;
+  static constexpr int kShares = kSolo ? kWarps : 1;               // shares of a CTA
+  static constexpr int kBlockTok = kTok * (kSolo ? 1 : kWarps);
   static constexpr int kScaleBytes = kFp8 ? 3 * kTok * 4 : 0;      // k scales; v scales, then their logarithms; reciprocals
 };
 
@@ -209,16 +211,17 @@ struct Walk {
   }
 };
 
-template <bool kFp8, int kDP, int kNQ>
+template <bool kFp8, int kDP, int kNQ, bool kSolo>
 struct Smem {
-  using G = Geo<kFp8, kDP, kNQ>;
+  using G = Geo<kFp8, kDP, kNQ, kSolo>;
+  static constexpr int kQPlaces = kSolo ? 2 * kWarps : 3;                             // two of each warp, or three of all
   static constexpr int kRows = 8 * kNQ, kDM = kDP / 16;
   static constexpr int kQRowBytes = kRows * kDP * 2;                                  // one unit's queries as they are
   static constexpr int kScaleOff = kWarps * G::kWarpBytes;                         // (the rings come first)
   static constexpr int kQOff = kScaleOff + kWarps * G::kStages * G::kScaleBytes;
-  static constexpr int kSumOff = kQOff + 3 * kQRowBytes;            // the warps' sum,
-  static constexpr int kMlOff = kSumOff + kNQ * kDM * 32 * 16;                        // and each row's maximum and sum
-  static constexpr int kScanOff = kMlOff + kNQ * 32 * 16;                             // one int64 per warp
+  static constexpr int kSumOff = kQOff + kQPlaces * kQRowBytes;            // the warps' sum,
+  static constexpr int kMlOff = kSumOff + (kSolo ? 0 : kNQ * kDM * 32 * 16);          // and each row's maximum and sum
+  static constexpr int kScanOff = kMlOff + (kSolo ? 0 : kNQ * 32 * 16);                             // one int64 per warp
   static constexpr int kTotal = kScanOff + 8 * kWarps;
 };
 
@@ -239,10 +242,10 @@ __device__ __forceinline__ float lse_of(float m, float l, float shift) {
   return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) - shift + log2f(l)) * 0.6931471805599453f;
 }
 
-template <bool kFp8, int kDP, int kNQ>
+template <bool kFp8, int kDP, int kNQ, bool kSolo>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
-  using G = Geo<kFp8, kDP, kNQ>;
-  using SM = Smem<kFp8, kDP, kNQ>;
+  using G = Geo<kFp8, kDP, kNQ, kSolo>;
+  using SM = Smem<kFp8, kDP, kNQ, kSolo>;
   constexpr int kTok = G::kTok, kKT = kTok / 16, kKS = kDP / 16, kDM = SM::kDM, kRows = SM::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128 - (sm100::smem_u32(smem_raw) & 127)) & 127);
@@ -254,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   float4* s_ml = reinterpret_cast<float4*>(smem + SM::kMlOff) + lane;
   __shared__ int s_any;
   int64_t* s_scan = reinterpret_cast<int64_t*>(smem + SM::kScanOff);
-  __shared__ int s_b;
-  __shared__ int64_t s_off;
+  __shared__ int s_b[G::kShares];
+  __shared__ int64_t s_off[G::kShares];
 
   // (this launch may begin while the one before it drains, and the join while this one does: each
   // waits here for all that ran before)
@@ -285,29 +288,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  const int64_t ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
-  const int64_t cta = blockIdx.x;
-  if (cta >= ctas) return;
-  const int64_t w0 = divide(cta * total, ctas), w1 = divide((cta + 1) * total, ctas);
-  if (mine > 0 && before <= w0 && w0 < before + mine) {
-    int64_t at = before;
-    for (int b = b_first; b < b_last; ++b) {
-      int lo, hi;
-      key_range(a, b, lo, hi, nullptr);
-      const int64_t n = (num_blocks<G::kBlockTok>(lo, hi) + kUnitCost) * units_per_seq;
-      if (w0 < at + n) {
-        s_b = b;
-        s_off = w0 - at;
-        break;
+  const int64_t shares = min(total, (int64_t)gridDim.x * G::kShares);
+  if ((int64_t)blockIdx.x * G::kShares >= shares) return;
+#pragma unroll 1
+  for (int k = 0; k < G::kShares; ++k) {
+    const int64_t first = divide(((int64_t)blockIdx.x * G::kShares + k) * total, shares);
+    if (mine > 0 && before <= first && first < before + mine) {
+      int64_t at = before;
+      for (int b = b_first; b < b_last; ++b) {
+        int lo, hi;
+        key_range(a, b, lo, hi, nullptr);
+        const int64_t n = (num_blocks<G::kBlockTok>(lo, hi) + kUnitCost) * units_per_seq;
+        if (first < at + n) {
+          s_b[k] = b;
+          s_off[k] = first - at;
+          break;
+        }
+        at += n;
       }
-      at += n;
     }
   }
   __syncthreads();
+  const int64_t share = (int64_t)blockIdx.x * G::kShares + (kSolo ? warp : 0);
+  if (share >= shares) return;
+  const int64_t w0 = divide(share * total, shares), w1 = divide((share + 1) * total, shares);
   Walk<G::kBlockTok> in, out;  // the pieces whose tiles this warp loads next, and computes next
   in.left = w1 - w0;
-  in.off = s_off;
-  in.next_b = s_b;
+  in.off = s_off[kSolo ? warp : 0];
+  in.next_b = s_b[kSolo ? warp : 0];
   out = in;
 
   const int page_mask = (1 << a.page_shift) - 1;
@@ -329,7 +337,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   const uint8_t* v_base = static_cast<const uint8_t*>(a.v_cache) + (ld_bytes ? 16 * ld_ch : 0);
   int stage_in = 0, stage_out = 0;
   int in_tok = 0, in_i = 0, in_end = 0, in_h = 0, page_next = 0;
-  int in_piece = -1, in_slot = 2, ahead = 0;  // the piece being loaded, its place for queries; tiles under way
+  constexpr int kPlaces = kSolo ? 2 : 3;  // for queries, used in turn
+  uint8_t* q_places = smem + SM::kQOff + (kSolo ? warp * 2 * SM::kQRowBytes : 0);
+  int in_piece = -1, in_slot = kPlaces - 1, ahead = 0;  // the piece being loaded, its place for queries; tiles under way
   bool in_more = true, in_first = false;
   // To the next tile, and the page numbers ahead of it.  Where a tile lies in one page, lane t holds
   // that of tile in_batch + t, 32 tiles from one load (a load per tile, waited for behind the copies
@@ -343,10 +353,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       in_more = in.next(a, units_per_seq);
       if (!in_more) return;
       ++in_piece;
-      in_slot = in_slot == 2 ? 0 : in_slot + 1;
+      in_slot = in_slot == kPlaces - 1 ? 0 : in_slot + 1;
       in_first = true;
       in_h = in.u / p.row_blocks;
-      in.tiles(warp, kTok, in_tok, in_i, in_end);
+      in.tiles(kSolo ? 0 : warp, kTok, in_tok, in_i, in_end);
       fresh = true;
     }
     if (!fresh) return;
@@ -367,13 +377,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       const uint32_t st = ring + stage_in * G::kStageBytes;
       if (in_first) {
         // the unit's queries come with its first tile: a load that is waited for at the unit's start
-        // would queue behind all the copies under way.  All four warps copy them (the same bytes); of
-        // three places the one behind a warp that lags and before one that leads is free.
+        // would queue behind all the copies under way.  All four warps of a shared unit copy them (the
+        // same bytes); of three places the one behind a warp that lags and before one that leads is free.
         in_first = false;
         constexpr int kQChunks = kDP * 2 / 16, kQPass = 32 / kQChunks;
         const int base = (in.u - in_h * p.row_blocks) * kRows, ch = lane % kQChunks;
         const int live = min(kRows, p.rows - base);
-        const uint32_t dst = sm100::smem_u32(smem + SM::kQOff + in_slot * SM::kQRowBytes);
+        const uint32_t dst = sm100::smem_u32(q_places + in_slot * SM::kQRowBytes);
         for (int r = lane / kQChunks; r < live; r += kQPass) {
           const int t = (base + r) / p.group, head = in_h * p.group + base + r - t * p.group;
           const __nv_bfloat16* src = a.q + (((int64_t)in.b * a.new_tokens + t) * a.hq + head) * a.d;
@@ -432,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     const int b = out.b, len = out.len, lo = out.lo, blk = out.blk, take = out.take, n_blk = out.n_blk, u = out.u;
     const int h = u / p.row_blocks, row_base = (u - h * p.row_blocks) * kRows;
     int tok0, i_begin, i_end;
-    out.tiles(warp, kTok, tok0, i_begin, i_end);
+    out.tiles(kSolo ? 0 : warp, kTok, tok0, i_begin, i_end);
     more = out.next(a, units_per_seq);
 
     // ---- the rows' key ranges, their queries as fragments.  A lane works on the scores of rows
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         rscale[nq][x] = base_scale;
       }
     auto make_fragments = [&]() {
-      const uint8_t* q_rows = smem + SM::kQOff + slot_out * SM::kQRowBytes;
+      const uint8_t* q_rows = q_places + slot_out * SM::kQRowBytes;
 #pragma unroll
       for (int nq = 0; nq < kNQ; ++nq) {
         const uint8_t* q_row = q_rows + (8 * nq + g) * (kDP * 2);
@@ -839,9 +849,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) l[nq][x] += __shfl_xor_sync(0xffffffffu, l[nq][x], sh);
-    if (warp > 0) sm100::named_bar(warp, 64);
-    else if (pieces > 0) sm100::named_bar(kWarps, 64);
-    const bool mine_any = i_begin < i_end, sum_any = warp > 0 && s_any;
+    // (A warp with a share of its own has the result already.)
+    if (!kSolo) {
+      if (warp > 0) sm100::named_bar(warp, 64);
+      else if (pieces > 0) sm100::named_bar(kWarps, 64);
+    }
+    const bool mine_any = i_begin < i_end, sum_any = !kSolo && warp > 0 && s_any;
     if (sum_any) {
 #pragma unroll
       for (int nq = 0; nq < kNQ; ++nq) {
@@ -867,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
     }
     __syncwarp();  // the sum has been read
-    if (warp < kWarps - 1) {
+    if (!kSolo && warp < kWarps - 1) {
       if (mine_any || warp == 0) {
 #pragma unroll
         for (int nq = 0; nq < kNQ; ++nq) {
@@ -880,8 +893,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       __syncwarp();
       sm100::named_bar_arrive(warp + 1, 64);
     } else {
-      if (more) sm100::named_bar_arrive(kWarps, 64);
-      const int64_t slot = 2 * cta + (pieces == 0 ? 0 : 1);
+      if (!kSolo && more) sm100::named_bar_arrive(kWarps, 64);
+      const int64_t slot = 2 * share + (pieces == 0 ? 0 : 1);
       if (blk == 0 && take == n_blk) {
 #pragma unroll
         for (int nq = 0; nq < kNQ; ++nq) {
@@ -911,24 +924,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
     }
     ++pieces;
-    slot_out = slot_out == 2 ? 0 : slot_out + 1;
+    slot_out = slot_out == kPlaces - 1 ? 0 : slot_out + 1;
   }
 }
 
-// Joins the partial results of every unit that more than one CTA worked on, in the order of its
+// Joins the partial results of every unit that more than one share has a part of, in the order of its
 // keys; fp32 sums.  The launch's blocks take jobs in turn: a row tile, its channel tiles a warp each, where a unit
 // has few partials; a row tile's one channel tile, the partials dealt to the eight warps, where it
 // has many.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kFewPartials = 8;
 
-template <bool kFp8, int kDP, int kNQ>
+template <bool kFp8, int kDP, int kNQ, bool kSolo>
 __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid_constant__ DecodeParams p, int grid) {
-  using G = Geo<kFp8, kDP, kNQ>;
-  constexpr int kDM = kDP / 16;
+  using G = Geo<kFp8, kDP, kNQ, kSolo>;
+  constexpr int kDM = kDP / 16, kMaxShares = kMaxCtas * G::kShares, kPer = (kMaxShares + kJoinThreads - 1) / kJoinThreads;
   const AttnDecodeArgs& a = p.a;
-  __shared__ int s_end[kMaxCtas];      // jobs up to and with the unit that CTA i ends
-  __shared__ int4 s_meta[kMaxCtas];    // that unit: first partial, partials, unit
+  __shared__ int s_end[kMaxShares];    // jobs up to and with the unit that share i ends
+  __shared__ int4 s_meta[kMaxShares];  // that unit: first partial, partials, unit
   __shared__ int s_warp[kJoinWarps];
   __shared__ int64_t s_sum[kJoinThreads];
   __shared__ float4 s_o[kJoinWarps][32], s_ml[kJoinWarps][32];
@@ -964,16 +977,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
   }
   s_sum[tid] = incl64;  // the cost up to and with this thread's sequences
   __syncthreads();
-  const int ctas = (int)min(cost, (int64_t)grid);
+  const int shares = (int)min(cost, (int64_t)grid * G::kShares);
   auto row_tiles = [&](int unit) { return min(kNQ, (p.rows - (unit % p.row_blocks) * 8 * kNQ + 7) / 8); };
-  int jobs[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int i = 2 * tid + k;
-    if (i >= ctas) continue;
-    // CTA i ends a unit that others began if its share begins inside that unit's blocks and goes on to
-    // their end
-    const int64_t w0 = divide(i * cost, ctas), w1 = divide((i + 1) * cost, ctas);
+  int jobs = 0;
+#pragma unroll 1
+  for (int k = 0; k < kPer; ++k) {
+    const int i = kPer * tid + k;
+    if (i >= shares) break;
+    // share i ends a unit that others began if it begins inside that unit's blocks and goes on to their end
+    const int64_t w0 = divide(i * cost, shares), w1 = divide((i + 1) * cost, shares);
     int lo = 0, hi = kJoinThreads - 1;  // the first thread whose sum is beyond w0
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -991,17 +1003,18 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
     const int u = (int)divide(w0 - at, n_cost), blk = (int)(w0 - at - (int64_t)u * n_cost);
     int4 mt = make_int4(0, 0, 0, 0);
     if (blk > 0 && blk < n_blk && w1 - w0 >= n_blk - blk) {
-      // the CTA of the unit's first block; the unit is that CTA's first one if its share begins there,
-      // or in the end (without blocks) of the unit before
+      // the share with the unit's first block; the unit is its first one if the share begins there, or in
+      // the end (without blocks) of the unit before
       const int64_t start = w0 - blk;
-      const int64_t c0 = divide((start + 1) * ctas - 1, cost);
-      mt = make_int4((int)(2 * c0 + (start - divide(c0 * cost, ctas) <= kUnitCost ? 0 : 1)), (int)(i - c0 + 1),
+      const int64_t c0 = divide((start + 1) * shares - 1, cost);
+      mt = make_int4((int)(2 * c0 + (start - divide(c0 * cost, shares) <= kUnitCost ? 0 : 1)), (int)(i - c0 + 1),
                      (int)((int64_t)b * units_per_seq + u), 0);
-      jobs[k] = row_tiles(mt.z) * (mt.y > kFewPartials ? kDM : 1);
+      jobs += row_tiles(mt.z) * (mt.y > kFewPartials ? kDM : 1);
     }
     s_meta[i] = mt;
+    s_end[i] = jobs;  // (of this thread's shares so far)
   }
-  int incl = jobs[0] + jobs[1];
+  int incl = jobs;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int t = __shfl_up_sync(0xffffffffu, incl, o);
@@ -1014,14 +1027,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
     if (w < warp) before += s_warp[w];
     total += s_warp[w];
   }
-  const int end1 = before + incl, end0 = end1 - jobs[1];
-  if (2 * tid < ctas) s_end[2 * tid] = end0;
-  if (2 * tid + 1 < ctas) s_end[2 * tid + 1] = end1;
+  for (int k = 0; k < kPer; ++k)
+    if (kPer * tid + k < shares) s_end[kPer * tid + k] += before + incl - jobs;
   __syncthreads();
   sm100::griddep_wait();
 
   for (int job = blockIdx.x; job < total; job += gridDim.x) {
-    int lo = 0, hi = ctas - 1;  // the first CTA whose end is beyond the job
+    int lo = 0, hi = shares - 1;  // the first share whose end is beyond the job
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (s_end[mid] > job) hi = mid;
@@ -1031,8 +1043,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
     const int local = job - (lo > 0 ? s_end[lo - 1] : 0);
     const bool many = mt.y > kFewPartials;
     const int nq = many ? local / kDM : local, jj = many ? local % kDM : warp;
-    const int cta0 = mt.x >> 1;
-    auto slot = [&](int i) { return (int64_t)(i == 0 ? mt.x : 2 * (cta0 + i)) * kNQ + nq; };
+    const int share0 = mt.x >> 1;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? mt.x : 2 * (share0 + i)) * kNQ + nq; };
     // partials first, first + step, ..: their results relative to the largest reference met so far
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
     auto add = [&](const float4& ml, const float4& t) {
@@ -1101,10 +1113,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
 int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
 int padded_dim(int d) { return d <= 64 ? 64 : 128; }
 
-template <bool kFp8, int kDP, int kNQ>
+template <bool kFp8, int kDP, int kNQ, bool kSolo>
 cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
-  using G = Geo<kFp8, kDP, kNQ>;
-  using SM = Smem<kFp8, kDP, kNQ>;
+  using G = Geo<kFp8, kDP, kNQ, kSolo>;
+  using SM = Smem<kFp8, kDP, kNQ, kSolo>;
   static bool attr_done[64] = {};
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
@@ -1118,13 +1130,14 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   const int64_t most_blocks = cap > G::kBlockTok ? (cap + G::kBlockTok - 1) / G::kBlockTok : 1;
   int64_t grid = (int64_t)kCtasPerSm * sms;
   if (grid > kMaxCtas) grid = kMaxCtas;
-  if (units < grid && units * (most_blocks + kUnitCost) < grid) grid = units * (most_blocks + kUnitCost);
+  const int64_t most_shares = units < grid * kWarps ? units * (most_blocks + kUnitCost) : INT64_MAX;
+  if (most_shares < grid * G::kShares) grid = (most_shares + G::kShares - 1) / G::kShares;
   uint8_t* ws = a.workspace;
   p.status = reinterpret_cast<uint32_t*>(ws);
   p.part_ml = reinterpret_cast<float4*>(ws + kWorkspaceHeader);
-  p.part_o = p.part_ml + 2 * kMaxCtas * kNQ * 32;
+  p.part_o = p.part_ml + 2 * kMaxCtas * kWarps * kNQ * 32;
   constexpr uint32_t kSmem = SM::kTotal + 128;
-  cudaError_t e = set_smem_once(attn_decode_kernel<kFp8, kDP, kNQ>, kSmem, attr_done);
+  cudaError_t e = set_smem_once(attn_decode_kernel<kFp8, kDP, kNQ, kSolo>, kSmem, attr_done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1136,27 +1149,35 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<kFp8, kDP, kNQ>, p);
+  e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<kFp8, kDP, kNQ, kSolo>, p);
   if (e != cudaSuccess || most_blocks == 1) return e;  // (no unit has two blocks: nothing to join)
   cfg.gridDim = dim3((unsigned)(2 * sms));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kFp8, kDP, kNQ>, p, (int)grid);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kFp8, kDP, kNQ, kSolo>, p, (int)grid);
 }
+
+// Units per warp from which warps take shares of their own: their results of a unit need no joining
+// then, but a unit is one warp's work.  (128 sequences, 8 kv heads, bf16: 80 rows, 5120 units, take 154 us
+// in common and 78 alone at 120 keys, 473 and 442 at 2000; 16 rows, 1024 units, take 35 and 41, 105 and 124.)
+constexpr int64_t kSoloUnits = 4;
 
 template <bool kFp8, int kDP>
 cudaError_t launch_rows(const AttnDecodeArgs& a, cudaStream_t stream) {
-  switch (row_tiles(a.new_tokens * (a.hq / a.hkv))) {
-    case 1: return launch_typed<kFp8, kDP, 1>(a, stream);
-    default: return launch_typed<kFp8, kDP, 2>(a, stream);
-  }
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int rows = a.new_tokens * (a.hq / a.hkv), tiles = row_tiles(rows);
+  const int64_t units = (int64_t)a.batch * a.hkv * ((rows + 8 * tiles - 1) / (8 * tiles));
+  if (units >= kSoloUnits * kWarps * kCtasPerSm * sms)
+    return tiles == 2 ? launch_typed<kFp8, kDP, 2, true>(a, stream) : launch_typed<kFp8, kDP, 1, true>(a, stream);
+  return tiles == 2 ? launch_typed<kFp8, kDP, 2, false>(a, stream) : launch_typed<kFp8, kDP, 1, false>(a, stream);
 }
 
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int32_t rows, int32_t d) {
   const size_t tiles = row_tiles(rows);
-  return kWorkspaceHeader + 2 * kMaxCtas * tiles * 32 * sizeof(float4) * (1 + padded_dim(d) / 16);
+  return kWorkspaceHeader + 2 * kMaxCtas * kWarps * tiles * 32 * sizeof(float4) * (1 + padded_dim(d) / 16);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream) {

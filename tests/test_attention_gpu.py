@@ -486,6 +486,47 @@ def test_decode_many_sequences(cuda_device):
     check_decode(lens, 1, 2, 1, 16, 8, False)
 
 
+@pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("d,new,group,window", [(64, 1, 1, 0), (128, 3, 2, 9), (128, 2, 6, 0), (48, 5, 5, 0)])
+def test_decode_very_many_units(cuda_device, d, new, group, window, quant):
+    """So many (sequence, kv head, rows) units that every warp takes a share of its own."""
+    gen = torch.Generator().manual_seed(19)
+    rows = new * group
+    blocks = -(-rows // (8 if rows <= 8 else 16))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    b = -(-4 * 4 * 2 * sms // (12 * blocks)) + 1
+    lens = torch.randint(0, 20, (b,), generator=gen).tolist()
+    lens[0], lens[b // 2], lens[-1] = 0, 300, 65
+    # (the formulas over a few of the sequences: the shortest, the longest, and some others)
+    gen2 = torch.Generator().manual_seed(11)
+    pages = sum(-(-n // 16) for n in lens) + 2
+    kc, ks = ref.make_cache(gen2, pages, 12, 16, d, quant)
+    vc, vs = ref.make_cache(gen2, pages, 12, 16, d, quant)
+    tab = ref.fill_sequences(gen2, lens, kc, vc, ks, vs)
+    q = torch.randn(b, new, 12 * group, d, generator=gen2).to(BF)
+    lse = torch.full(q.shape[:3], 99.0, device="cuda")
+    ksd, vsd = dev(ks, vs)
+    args = [t.cuda() for t in (q, kc, vc, tab, torch.tensor(lens, dtype=torch.int32))]
+    out = kda.attn_decode(*args, 0.2, lse=lse, k_scale=ksd, v_scale=vsd, window=window)
+    pick = sorted({0, 1, 2, b // 3, b // 2, b // 2 + 1, b - 2, b - 1})
+    o, l, ot, lt = ref.attention(q[pick], kc, vc, tab[pick], [lens[i] for i in pick], 0.2, ks, vs, 0.0, window)
+    within(out.cpu()[pick], o, ot, "out")
+    within(lse.cpu()[pick], l, lt, "lse")
+    # every other row: the call gives the same with the sequences one by one in a small batch
+    few = torch.arange(3, b, max(1, b // 40))
+    small = kda.attn_decode(args[0][few], args[1], args[2], args[3][few].contiguous(), args[4][few].contiguous(), 0.2, k_scale=ksd,
+                            v_scale=vsd, window=window)
+    # (the two forms add the same terms in other orders: a rounding of the result, and 2^-9 of P V's size)
+    a, c = out[few].float(), small.float()
+    assert ((a - c).abs() <= 2 * ref.BF16 * c.abs() + 2.0 ** -9 * vsize(vc, vs)).all()
+
+
+def vsize(vc, vs):
+    """The largest magnitude of a written value."""
+    v = vc.float() if vs is None else vc.float() * vs[..., None]
+    return float(v[torch.isfinite(v)].abs().max())
+
+
 def test_decode_lengths_and_pages_out_of_range(cuda_device):
     gen = torch.Generator().manual_seed(2)
     kc, _ = ref.make_cache(gen, 8, 1, 16, 64, False)
