@@ -17,8 +17,8 @@
 //     also across the ends of units; about 130 KB of copies in flight per SM.  (TMA boxes instead cost
 //     the issuing warp 800 to 900 cycles a tile, four boxes each, of 2600 to 3400.)
 //   - The warps' results of a unit meet as a chain through shared memory, so that no warp waits for a
-//     slower one before it goes on with the next unit.  With very many units (kSolo) each warp takes a
-//     share of its own instead.
+//     slower one before it goes on with the next unit.  With very many units each warp takes a share of
+//     its own instead; few short units are not split at all.
 //   - The products are transposed, S^T = K Q^T and O^T = V^T P^T, mma.sync m16n8k16 with the keys (the
 //     channels) as the 16 and 8 rows of queries as the 8: a unit of up to 8 rows (one kv head's group
 //     at T = 1) wastes half as much of each instruction, and half the registers, as with 16 rows.
@@ -38,10 +38,13 @@
 namespace kda {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kCtasPerSm = 2;
+// How the work is dealt out: equal shares of all blocks to the CTAs (kCommon), or to their warps, where
+// units are very many (kSolo); or each unit to one CTA, where they are few and short (kWhole).
+enum Mode { kCommon, kSolo, kWhole };
+
+constexpr int kCtasPerSm = 2;               // (kWhole: one of twice the warps)
 constexpr int kMaxCtas = kCtasPerSm * 160;  // bound used for the workspace (148 SMs on a B200)
+constexpr int kMaxShares = kMaxCtas * 4;    // (kSolo)
 constexpr float kLazy = 8.0f;         // how far (base 2) a score passes a row's reference before it moves
 constexpr float kWeightShift = 7.0f;  // fp16 weights: up to 2^(kLazy + kWeightShift) = 2^15
 
@@ -126,8 +129,11 @@ __device__ __forceinline__ float tanh_any(float x) {
 // together (4 KB for 64 e4m3 channels); a block is one tile per warp.  Two CTAs of 4 warps per SM:
 // their registers allow no more beyond 8 rows; up to 8, more warps (two CTAs of 6, three of 4) were no
 // faster for long sequences and slower for short ones.  The bf16 cache has room for a third stage there.
-template <bool kFp8, int kDP, int kNQ, bool kSolo>
+template <bool kFp8, int kDP, int kNQ, Mode kMode>
 struct Geo {
+  static constexpr int kWarps = kMode == kWhole ? 8 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCtas = kMode == kWhole ? 1 : kCtasPerSm;   // per SM
   static constexpr int kTok = kFp8 ? 32 : (kDP == 128 ? 16 : 32);
   static constexpr int kRowBytes = kFp8 ? kDP : 128;               // bytes of a row in one column block
   static constexpr int kColBlocks = kFp8 ? 1 : kDP / 64;           // 128-byte column blocks (bf16)
@@ -135,8 +141,8 @@ struct Geo {
   static constexpr int kStageBytes = 2 * kOpBytes;
   static constexpr int kWarpBytes = kNQ == 1 && !kFp8 ? 24576 : 16384;
   static constexpr int kStages = kWarpBytes / kStageBytes;
-  static constexpr int kShares = kSolo ? kWarps : 1;               // shares of a CTA
-  static constexpr int kBlockTok = kTok * (kSolo ? 1 : kWarps);
+  static constexpr int kShares = kMode == kSolo ? kWarps : 1;      // shares of a CTA
+  static constexpr int kBlockTok = kTok * (kMode == kSolo ? 1 : kWarps);
   static constexpr int kScaleBytes = kFp8 ? 3 * kTok * 4 : 0;      // k scales; v scales, then their logarithms; reciprocals
 };
 
@@ -211,17 +217,18 @@ struct Walk {
   }
 };
 
-template <bool kFp8, int kDP, int kNQ, bool kSolo>
+template <bool kFp8, int kDP, int kNQ, Mode kMode>
 struct Smem {
-  using G = Geo<kFp8, kDP, kNQ, kSolo>;
-  static constexpr int kQPlaces = kSolo ? 2 * kWarps : 3;                             // two of each warp, or three of all
+  using G = Geo<kFp8, kDP, kNQ, kMode>;
+  static constexpr int kWarps = G::kWarps;
+  static constexpr int kQPlaces = kMode == kSolo ? 2 * kWarps : 3;                             // two of each warp, or three of all
   static constexpr int kRows = 8 * kNQ, kDM = kDP / 16;
   static constexpr int kQRowBytes = kRows * kDP * 2;                                  // one unit's queries as they are
   static constexpr int kScaleOff = kWarps * G::kWarpBytes;                         // (the rings come first)
   static constexpr int kQOff = kScaleOff + kWarps * G::kStages * G::kScaleBytes;
   static constexpr int kSumOff = kQOff + kQPlaces * kQRowBytes;            // the warps' sum,
-  static constexpr int kMlOff = kSumOff + (kSolo ? 0 : kNQ * kDM * 32 * 16);          // and each row's maximum and sum
-  static constexpr int kScanOff = kMlOff + (kSolo ? 0 : kNQ * 32 * 16);                             // one int64 per warp
+  static constexpr int kMlOff = kSumOff + (kMode == kSolo ? 0 : kNQ * kDM * 32 * 16);          // and each row's maximum and sum
+  static constexpr int kScanOff = kMlOff + (kMode == kSolo ? 0 : kNQ * 32 * 16);                             // one int64 per warp
   static constexpr int kTotal = kScanOff + 8 * kWarps;
 };
 
@@ -242,10 +249,12 @@ __device__ __forceinline__ float lse_of(float m, float l, float shift) {
   return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) - shift + log2f(l)) * 0.6931471805599453f;
 }
 
-template <bool kFp8, int kDP, int kNQ, bool kSolo>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
-  using G = Geo<kFp8, kDP, kNQ, kSolo>;
-  using SM = Smem<kFp8, kDP, kNQ, kSolo>;
+template <bool kFp8, int kDP, int kNQ, Mode kMode>
+__global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8, kDP, kNQ, kMode>::kCtas)
+    attn_decode_kernel(const __grid_constant__ DecodeParams p) {
+  using G = Geo<kFp8, kDP, kNQ, kMode>;
+  using SM = Smem<kFp8, kDP, kNQ, kMode>;
+  constexpr int kWarps = G::kWarps, kThreads = G::kThreads;
   constexpr int kTok = G::kTok, kKT = kTok / 16, kKS = kDP / 16, kDM = SM::kDM, kRows = SM::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128 - (sm100::smem_u32(smem_raw) & 127)) & 127);
@@ -265,57 +274,73 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
 
-  // ---- this CTA's share [w0, w1) of all blocks, and the sequence it begins in
   const int64_t units_per_seq = (int64_t)a.hkv * p.row_blocks;
-  const int per = (a.batch + kThreads - 1) / kThreads;
-  const int b_first = tid * per, b_last = min(a.batch, b_first + per);
-  int64_t mine = 0;
-  for (int b = b_first; b < b_last; ++b) {
-    int lo, hi;
-    key_range(a, b, lo, hi, blockIdx.x == 0 ? p.status : nullptr);
-    mine += (num_blocks<G::kBlockTok>(lo, hi) + kUnitCost) * units_per_seq;
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - mine, total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-  }
-  const int64_t shares = min(total, (int64_t)gridDim.x * G::kShares);
-  if ((int64_t)blockIdx.x * G::kShares >= shares) return;
-#pragma unroll 1
-  for (int k = 0; k < G::kShares; ++k) {
-    const int64_t first = divide(((int64_t)blockIdx.x * G::kShares + k) * total, shares);
-    if (mine > 0 && before <= first && first < before + mine) {
-      int64_t at = before;
-      for (int b = b_first; b < b_last; ++b) {
+  Walk<G::kBlockTok> in, out;  // the pieces whose tiles this warp loads next, and computes next
+  int64_t share = blockIdx.x;
+  if (kMode == kWhole) {
+    // (the lengths of all sequences are only looked at for the status)
+    if (blockIdx.x == 0)
+      for (int b = tid; b < a.batch; b += kThreads) {
         int lo, hi;
-        key_range(a, b, lo, hi, nullptr);
-        const int64_t n = (num_blocks<G::kBlockTok>(lo, hi) + kUnitCost) * units_per_seq;
-        if (first < at + n) {
-          s_b[k] = b;
-          s_off[k] = first - at;
-          break;
+        key_range(a, b, lo, hi, p.status);
+      }
+    in.next_b = (int)(share / units_per_seq);
+    int lo, hi;
+    key_range(a, in.next_b, lo, hi, nullptr);
+    in.left = num_blocks<G::kBlockTok>(lo, hi);
+    in.off = (share - in.next_b * units_per_seq) * (in.left + kUnitCost);
+    if (tid == 0) s_any = 0;
+    __syncthreads();
+  } else {
+    // ---- this CTA's share [w0, w1) of all blocks, and the sequence it begins in
+    const int per = (a.batch + kThreads - 1) / kThreads;
+    const int b_first = tid * per, b_last = min(a.batch, b_first + per);
+    int64_t mine = 0;
+    for (int b = b_first; b < b_last; ++b) {
+      int lo, hi;
+      key_range(a, b, lo, hi, blockIdx.x == 0 ? p.status : nullptr);
+      mine += (num_blocks<G::kBlockTok>(lo, hi) + kUnitCost) * units_per_seq;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    const int64_t shares = min(total, (int64_t)gridDim.x * G::kShares);
+    if ((int64_t)blockIdx.x * G::kShares >= shares) return;
+#pragma unroll 1
+    for (int k = 0; k < G::kShares; ++k) {
+      const int64_t first = divide(((int64_t)blockIdx.x * G::kShares + k) * total, shares);
+      if (mine > 0 && before <= first && first < before + mine) {
+        int64_t at = before;
+        for (int b = b_first; b < b_last; ++b) {
+          int lo, hi;
+          key_range(a, b, lo, hi, nullptr);
+          const int64_t n = (num_blocks<G::kBlockTok>(lo, hi) + kUnitCost) * units_per_seq;
+          if (first < at + n) {
+            s_b[k] = b;
+            s_off[k] = first - at;
+            break;
+          }
+          at += n;
         }
-        at += n;
       }
     }
+    __syncthreads();
+    share = (int64_t)blockIdx.x * G::kShares + (kMode == kSolo ? warp : 0);
+    if (share >= shares) return;
+    in.left = divide((share + 1) * total, shares) - divide(share * total, shares);
+    in.off = s_off[kMode == kSolo ? warp : 0];
+    in.next_b = s_b[kMode == kSolo ? warp : 0];
   }
-  __syncthreads();
-  const int64_t share = (int64_t)blockIdx.x * G::kShares + (kSolo ? warp : 0);
-  if (share >= shares) return;
-  const int64_t w0 = divide(share * total, shares), w1 = divide((share + 1) * total, shares);
-  Walk<G::kBlockTok> in, out;  // the pieces whose tiles this warp loads next, and computes next
-  in.left = w1 - w0;
-  in.off = s_off[kSolo ? warp : 0];
-  in.next_b = s_b[kSolo ? warp : 0];
   out = in;
 
   const int page_mask = (1 << a.page_shift) - 1;
@@ -337,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   const uint8_t* v_base = static_cast<const uint8_t*>(a.v_cache) + (ld_bytes ? 16 * ld_ch : 0);
   int stage_in = 0, stage_out = 0;
   int in_tok = 0, in_i = 0, in_end = 0, in_h = 0, page_next = 0;
-  constexpr int kPlaces = kSolo ? 2 : 3;  // for queries, used in turn
-  uint8_t* q_places = smem + SM::kQOff + (kSolo ? warp * 2 * SM::kQRowBytes : 0);
+  constexpr int kPlaces = kMode == kSolo ? 2 : 3;  // for queries, used in turn
+  uint8_t* q_places = smem + SM::kQOff + (kMode == kSolo ? warp * 2 * SM::kQRowBytes : 0);
   int in_piece = -1, in_slot = kPlaces - 1, ahead = 0;  // the piece being loaded, its place for queries; tiles under way
   bool in_more = true, in_first = false;
   // To the next tile, and the page numbers ahead of it.  Where a tile lies in one page, lane t holds
@@ -356,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       in_slot = in_slot == kPlaces - 1 ? 0 : in_slot + 1;
       in_first = true;
       in_h = in.u / p.row_blocks;
-      in.tiles(kSolo ? 0 : warp, kTok, in_tok, in_i, in_end);
+      in.tiles(kMode == kSolo ? 0 : warp, kTok, in_tok, in_i, in_end);
       fresh = true;
     }
     if (!fresh) return;
@@ -442,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     const int b = out.b, len = out.len, lo = out.lo, blk = out.blk, take = out.take, n_blk = out.n_blk, u = out.u;
     const int h = u / p.row_blocks, row_base = (u - h * p.row_blocks) * kRows;
     int tok0, i_begin, i_end;
-    out.tiles(kSolo ? 0 : warp, kTok, tok0, i_begin, i_end);
+    out.tiles(kMode == kSolo ? 0 : warp, kTok, tok0, i_begin, i_end);
     more = out.next(a, units_per_seq);
 
     // ---- the rows' key ranges, their queries as fragments.  A lane works on the scores of rows
@@ -849,12 +874,56 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) l[nq][x] += __shfl_xor_sync(0xffffffffu, l[nq][x], sh);
-    // (A warp with a share of its own has the result already.)
-    if (!kSolo) {
+    // (A warp with a share of its own has the result already.  With one unit per CTA nothing is to go on
+    // with: the warps lay their sums side by side over the rings, and each adds up a channel tile.)
+    if (kMode == kWhole) {
+      float4* mine = reinterpret_cast<float4*>(stages) + lane;
+#pragma unroll
+      for (int nq = 0; nq < kNQ; ++nq) {
+        mine[(kNQ * kDM + nq) * 32] = make_float4(m[nq][0], l[nq][0], m[nq][1], l[nq][1]);
+#pragma unroll
+        for (int j = 0; j < kDM; ++j) mine[(nq * kDM + j) * 32] = make_float4(o[nq][j][0], o[nq][j][1], o[nq][j][2], o[nq][j][3]);
+      }
+      __syncthreads();
+      if (warp >= kDM) break;
+      const float4* all = reinterpret_cast<const float4*>(smem) + lane;
+      constexpr int kStep = G::kWarpBytes / 16;
+#pragma unroll
+      for (int nq = 0; nq < kNQ; ++nq) {
+        float4 ml[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) ml[w] = all[w * kStep + (kNQ * kDM + nq) * 32];
+        float top[2] = {-INFINITY, -INFINITY}, sum_l[2] = {}, sum_o[4] = {};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top[0] = fmaxf(top[0], ml[w].x), top[1] = fmaxf(top[1], ml[w].z);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 t = all[w * kStep + (nq * kDM + warp) * 32];
+          const float f0 = ml[w].x == -INFINITY ? 1.f : ex2_approx(ml[w].x - top[0]);  // (as below)
+          const float f1 = ml[w].z == -INFINITY ? 1.f : ex2_approx(ml[w].z - top[1]);
+          sum_l[0] += ml[w].y * f0, sum_l[1] += ml[w].w * f1;
+          sum_o[0] += t.x * f0, sum_o[1] += t.y * f1, sum_o[2] += t.z * f0, sum_o[3] += t.w * f1;
+        }
+        const int row = row_base + 8 * nq + g, t = row / p.group;
+        __nv_bfloat16* row_out = nullptr;
+        if (row < p.rows) row_out = a.out + (((int64_t)b * a.new_tokens + t) * a.hq + h * p.group + row - t * p.group) * a.d;
+        float inv[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          inv[x] = sum_l[x] == 0.f ? 0.f : 1.f / sum_l[x];
+          const int r = row_base + 8 * nq + 2 * c + x, rt = r / p.group;
+          if (warp == 0 && g == 0 && r < p.rows && a.lse)
+            a.lse[((int64_t)b * a.new_tokens + rt) * a.hq + h * p.group + r - rt * p.group] = lse_of(top[x], sum_l[x], kFp8 ? kWeightShift : 0.f);
+        }
+        write_tile<kFp8, kDP>(sum_o, warp, inv, row_out, a.d);
+      }
+      break;
+    }
+    if (kMode != kSolo) {
       if (warp > 0) sm100::named_bar(warp, 64);
       else if (pieces > 0) sm100::named_bar(kWarps, 64);
     }
-    const bool mine_any = i_begin < i_end, sum_any = !kSolo && warp > 0 && s_any;
+    const bool mine_any = i_begin < i_end, sum_any = kMode != kSolo && warp > 0 && s_any;
     if (sum_any) {
 #pragma unroll
       for (int nq = 0; nq < kNQ; ++nq) {
@@ -880,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
     }
     __syncwarp();  // the sum has been read
-    if (!kSolo && warp < kWarps - 1) {
+    if (kMode != kSolo && warp < kWarps - 1) {
       if (mine_any || warp == 0) {
 #pragma unroll
         for (int nq = 0; nq < kNQ; ++nq) {
@@ -893,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       __syncwarp();
       sm100::named_bar_arrive(warp + 1, 64);
     } else {
-      if (!kSolo && more) sm100::named_bar_arrive(kWarps, 64);
+      if (kMode != kSolo && more) sm100::named_bar_arrive(kWarps, 64);
       const int64_t slot = 2 * share + (pieces == 0 ? 0 : 1);
       if (blk == 0 && take == n_blk) {
 #pragma unroll
@@ -935,13 +1004,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kFewPartials = 8;
 
-template <bool kFp8, int kDP, int kNQ, bool kSolo>
+template <bool kFp8, int kDP, int kNQ, Mode kMode>
 __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid_constant__ DecodeParams p, int grid) {
-  using G = Geo<kFp8, kDP, kNQ, kSolo>;
-  constexpr int kDM = kDP / 16, kMaxShares = kMaxCtas * G::kShares, kPer = (kMaxShares + kJoinThreads - 1) / kJoinThreads;
+  using G = Geo<kFp8, kDP, kNQ, kMode>;
+  constexpr int kDM = kDP / 16, kMost = kMaxCtas * G::kShares, kPer = (kMost + kJoinThreads - 1) / kJoinThreads;
   const AttnDecodeArgs& a = p.a;
-  __shared__ int s_end[kMaxShares];    // jobs up to and with the unit that share i ends
-  __shared__ int4 s_meta[kMaxShares];  // that unit: first partial, partials, unit
+  __shared__ int s_end[kMost];    // jobs up to and with the unit that share i ends
+  __shared__ int4 s_meta[kMost];  // that unit: first partial, partials, unit
   __shared__ int s_warp[kJoinWarps];
   __shared__ int64_t s_sum[kJoinThreads];
   __shared__ float4 s_o[kJoinWarps][32], s_ml[kJoinWarps][32];
@@ -1113,10 +1182,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
 int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
 int padded_dim(int d) { return d <= 64 ? 64 : 128; }
 
-template <bool kFp8, int kDP, int kNQ, bool kSolo>
+template <bool kFp8, int kDP, int kNQ, Mode kMode>
 cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
-  using G = Geo<kFp8, kDP, kNQ, kSolo>;
-  using SM = Smem<kFp8, kDP, kNQ, kSolo>;
+  using G = Geo<kFp8, kDP, kNQ, kMode>;
+  using SM = Smem<kFp8, kDP, kNQ, kMode>;
   static bool attr_done[64] = {};
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
@@ -1130,54 +1199,68 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   const int64_t most_blocks = cap > G::kBlockTok ? (cap + G::kBlockTok - 1) / G::kBlockTok : 1;
   int64_t grid = (int64_t)kCtasPerSm * sms;
   if (grid > kMaxCtas) grid = kMaxCtas;
-  const int64_t most_shares = units < grid * kWarps ? units * (most_blocks + kUnitCost) : INT64_MAX;
+  const int64_t most_shares = units < grid * G::kWarps ? units * (most_blocks + kUnitCost) : INT64_MAX;
   if (most_shares < grid * G::kShares) grid = (most_shares + G::kShares - 1) / G::kShares;
+  if (kMode == kWhole) grid = units;
   uint8_t* ws = a.workspace;
   p.status = reinterpret_cast<uint32_t*>(ws);
   p.part_ml = reinterpret_cast<float4*>(ws + kWorkspaceHeader);
-  p.part_o = p.part_ml + 2 * kMaxCtas * kWarps * kNQ * 32;
+  p.part_o = p.part_ml + 2 * kMaxShares * kNQ * 32;
   constexpr uint32_t kSmem = SM::kTotal + 128;
-  cudaError_t e = set_smem_once(attn_decode_kernel<kFp8, kDP, kNQ, kSolo>, kSmem, attr_done);
+  cudaError_t e = set_smem_once(attn_decode_kernel<kFp8, kDP, kNQ, kMode>, kSmem, attr_done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(G::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<kFp8, kDP, kNQ, kSolo>, p);
-  if (e != cudaSuccess || most_blocks == 1) return e;  // (no unit has two blocks: nothing to join)
+  e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<kFp8, kDP, kNQ, kMode>, p);
+  if (e != cudaSuccess || kMode == kWhole || most_blocks == 1) return e;  // (no unit is in two shares: nothing to join)
   cfg.gridDim = dim3((unsigned)(2 * sms));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kFp8, kDP, kNQ, kSolo>, p, (int)grid);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kFp8, kDP, kNQ, kMode>, p, (int)grid);
 }
 
 // Units per warp from which warps take shares of their own: their results of a unit need no joining
 // then, but a unit is one warp's work.  (128 sequences, 8 kv heads, bf16: 80 rows, 5120 units, take 154 us
 // in common and 78 alone at 120 keys, 473 and 442 at 2000; 16 rows, 1024 units, take 35 and 41, 105 and 124.)
 constexpr int64_t kSoloUnits = 4;
+// Keys in the tables up to which units that all find an SM are not split: one launch, no join, but a
+// unit is one CTA's work.  The more units there are, the less splitting them helps; lengths that differ
+// are what the second bound is for.  (bf16, 4 rows of 128 channels, split and whole: 8 units take 9.8 and
+// 7.3 us at 333 keys, 10.1 and 10.1 at 760, 11.1 and 15.2 at 1500; 128 units 13.8 and 8.0, 16.9 and 10.8, 18.3 and
+// 15.5.  16 rows, 8 units: 12.5 and 9.8, 11.4 and 12.9.)
+constexpr int64_t kWholeKeys = 640, kWholeMost = 1024;
+
+template <bool kFp8, int kDP, int kNQ>
+cudaError_t launch_mode(const AttnDecodeArgs& a, int64_t units, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  if (units >= kSoloUnits * Geo<kFp8, kDP, kNQ, kCommon>::kWarps * kCtasPerSm * sms) return launch_typed<kFp8, kDP, kNQ, kSolo>(a, stream);
+  const int64_t keys = (int64_t)a.max_pages << a.page_shift;
+  if (units <= sms && keys <= kWholeMost && keys * (sms - units) <= kWholeKeys * sms)
+    return launch_typed<kFp8, kDP, kNQ, kWhole>(a, stream);
+  return launch_typed<kFp8, kDP, kNQ, kCommon>(a, stream);
+}
 
 template <bool kFp8, int kDP>
 cudaError_t launch_rows(const AttnDecodeArgs& a, cudaStream_t stream) {
-  const int sms = sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
   const int rows = a.new_tokens * (a.hq / a.hkv), tiles = row_tiles(rows);
   const int64_t units = (int64_t)a.batch * a.hkv * ((rows + 8 * tiles - 1) / (8 * tiles));
-  if (units >= kSoloUnits * kWarps * kCtasPerSm * sms)
-    return tiles == 2 ? launch_typed<kFp8, kDP, 2, true>(a, stream) : launch_typed<kFp8, kDP, 1, true>(a, stream);
-  return tiles == 2 ? launch_typed<kFp8, kDP, 2, false>(a, stream) : launch_typed<kFp8, kDP, 1, false>(a, stream);
+  return tiles == 2 ? launch_mode<kFp8, kDP, 2>(a, units, stream) : launch_mode<kFp8, kDP, 1>(a, units, stream);
 }
 
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int32_t rows, int32_t d) {
   const size_t tiles = row_tiles(rows);
-  return kWorkspaceHeader + 2 * kMaxCtas * kWarps * tiles * 32 * sizeof(float4) * (1 + padded_dim(d) / 16);
+  return kWorkspaceHeader + 2 * (size_t)kMaxShares * tiles * 32 * sizeof(float4) * (1 + padded_dim(d) / 16);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream) {
