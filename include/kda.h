@@ -339,8 +339,8 @@ kda_status_t kda_bwd(const void* q, const void* k, const void* v, const void* g,
  *   cos_sin     fp32 [max_positions][rot_dim]: the cosines of a position's rot_dim / 2 angles, then
  *               the sines; rot_dim a multiple of 16 up to D, 0 for no rotation (table and positions unused)
  *   positions   int32 [tokens]
- * Either of q and k may be left out (num_q_heads or num_kv_heads 0).  In place (q_out = q, k_out = k)
- * where the input is contiguous. */
+ * (A row's sum of squares is fp32: it must be below 2^128.)  Either of q and k may be left out
+ * (num_q_heads or num_kv_heads 0).  In place (q_out = q, k_out = k) where the input is contiguous. */
 kda_status_t kda_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
                               const float* q_weight, const float* k_weight, float eps, const float* cos_sin,
                               const int32_t* positions, void* q_out, void* k_out, int64_t tokens,
@@ -364,8 +364,9 @@ kda_status_t kda_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, cons
                                   void* workspace, size_t workspace_bytes, kda_stream_t stream);
 
 /* kda_qk_norm_rope with the keys, and the values as they are, written to the cache: token t's rows to
- * slots[t] (int32).  A negative slot skips its token (padding: nothing of it is read or written, q_out
- * included); the non-negative slots of a call must be distinct.  q may be left out (num_q_heads 0).
+ * slots[t] (int32).  A negative slot skips its token (padding: nothing of it is written, q_out included,
+ * and neither its position nor its rows' contents matter); the non-negative slots of a call must be
+ * distinct.  q may be left out (num_q_heads 0).
  * An e4m3 row gets scale = max(max_c |x_c| / 448, 2^-64) and codes round(x / scale) of its fp32
  * values; a row that holds an infinity or NaN gets the scale NaN and codes 0, so it reads as NaN. */
 kda_status_t kda_kv_append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
@@ -401,13 +402,15 @@ size_t kda_attn_decode_workspace_size(int32_t new_tokens, int32_t num_q_heads, i
  * A query that sees no key (a length of 0, or fewer tokens than new_tokens) gets out = 0 and lse = -inf.
  * Whatever the rows a query does not see hold, NaN included, does not reach it, except for e4m3 codes
  * that are NaN themselves in rows that some other query of the sequence sees (kda_kv_append writes none).
+ * An infinity or NaN in a row that it sees gives NaN or an infinity where the formula has either (with an
+ * e4m3 cache in lse too).
  *   q, out      bf16 [batch][new_tokens][num_q_heads][D] (out not in q's place);  lse fp32
  *               [batch][new_tokens][num_q_heads] or NULL
  *   page_table  int32 [batch][max_pages] (max_pages * page_size <= 2^30), seq_lens int32 [batch].
  *               Sequences may share pages.  With a window, entries of pages before it are not read.
  *   workspace   kda_attn_decode_workspace_size bytes, 256-byte aligned; calls that share one must be
  *               ordered (the same stream, or events).
- * One pass over the cache in two launches (one, where no sequence can be longer than a piece); fp32
+ * One pass over the cache in two launches (one, where few sequences can have few keys each); fp32
  * scores, softmax statistics and sums.  The order of all sums is fixed by the sizes and lengths. */
 kda_status_t kda_attn_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                              const float* v_scale, const int32_t* page_table, const int32_t* seq_lens, float scale,

@@ -43,7 +43,7 @@ kda_status_t check_cache(const void* k_cache, const void* v_cache, const float* 
   if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return KDA_ERR_INVALID_ARGUMENT;
   if ((k_scale == nullptr) != (v_scale == nullptr) || !aligned(k_scale, 4) || !aligned(v_scale, 4)) return KDA_ERR_INVALID_ARGUMENT;
   const int64_t page = (int64_t)hkv * page_size * d, align = k_scale ? 16 : 8;
-  // (the strides in bytes stay below 2^40, the limit of the tensor maps the reads go through)
+  // (2^38 elements are beyond any memory: a stride by mistake)
   for (int64_t s : {k_page_stride, v_page_stride})
     if (s < page || s % align != 0 || s >= (int64_t)1 << 38) return KDA_ERR_INVALID_ARGUMENT;
   return KDA_OK;
@@ -244,7 +244,7 @@ kda_status_t kda_attn_decode(const void* q, const void* k_cache, const void* v_c
   if (!isfinite(scale) || !(softcap >= 0.f && isfinite(softcap)) || (softcap > 0.f && !isfinite(scale / softcap)))
     return KDA_ERR_INVALID_ARGUMENT;
   const int64_t rows = (int64_t)new_tokens * (num_q_heads / num_kv_heads);
-  // (rows, units and the rows' indexes are int32; a unit is a sequence's kv head and 16 or 32 of its rows)
+  // (rows, units and the rows' indexes are int32; a unit is a sequence's kv head and 8 or 16 of its rows)
   if (rows > 1 << 20 || (int64_t)batch * num_kv_heads > INT32_MAX / (rows / 16 + 1) ||
       (int64_t)batch * new_tokens > INT32_MAX / num_q_heads)
     return KDA_ERR_INVALID_ARGUMENT;

@@ -26,9 +26,10 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;     // of the gradient and the cache read
-constexpr int kRopeThreads = 128; // of the forward: the smaller blocks end more evenly
-constexpr int kRows = 4;      // rows of one token that a group of lanes takes at a time
-constexpr int kReadRows = 8;  // cache rows likewise
+constexpr int kRopeThreads = 64;  // of the forward: the smaller blocks end more evenly,
+constexpr int kRopeCtas = 8;      // this many per SM
+constexpr int kRows = 4;          // rows of one token that a group of lanes takes at a time
+constexpr int kReadRows = 8;      // cache rows likewise
 
 // Two fp32 values in a 64-bit register, for the packed fp32 instructions.
 typedef unsigned long long F2;
@@ -201,139 +202,168 @@ __device__ __forceinline__ uint2 e4m3_codes(const Row8& x, float scale) {
   return make_uint2(w[0], w[1]);
 }
 
-// A group of lanes takes `batches` times kRows heads of one token and kind (q, k, v), one read of the
-// token's angles and the weights for all, the next rows' loads under way while it works on these.
+// A group of lanes takes `batches` times kRows heads of one token and kind (q, k, v) as an item, one read
+// of the token's angles and the weights for all, the next rows' loads under way while it works on these.
+// kLoop: more items than groups of a full device; a group then takes several in turn, the next one's
+// indexes and first rows under way too (32768 tokens of 96 + 12 heads: 327 us without, 293 with; a few
+// tokens, which need neither, 3.7 us with and 3.3 without).
 // kAppend: k and v go to the cache, and a negative slot skips its token; else k goes to k_out.
-template <int kLanes, bool kAppend, bool kQuant>
-__global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid_constant__ RopeArgs a, int batches) {
+template <int kLanes, bool kAppend, bool kQuant, bool kLoop>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(const __grid_constant__ RopeArgs a, int batches) {
   const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1);
   const int rows = kRows * batches;
   const int nq = (a.q.heads + rows - 1) / rows, nk = (a.k.heads + rows - 1) / rows, nv = (a.v.heads + rows - 1) / rows;
-  const int per_token = nq + nk + nv;
-  const uint32_t item = blockIdx.x * (kRopeThreads / kLanes) + threadIdx.x / kLanes;  // (below 2^31: checked by the host)
-  const int64_t token = item / (uint32_t)per_token;
-  bool live = token < a.tokens;  // (every lane stays for the shuffles)
-  const int part = (int)(item % (uint32_t)per_token);
-  const int kind = part < nq ? 0 : part < nq + nk ? 1 : 2;
-  HeadRows in;
-  in.x = kind == 0 ? a.q.x : kind == 1 ? a.k.x : a.v.x;
-  in.stride = kind == 0 ? a.q.stride : kind == 1 ? a.k.stride : a.v.stride;
-  in.heads = kind == 0 ? a.q.heads : kind == 1 ? a.k.heads : a.v.heads;
-  in.w = kind == 0 ? a.q.w : kind == 1 ? a.k.w : nullptr;
-  int head0 = (part - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * rows;
-  const bool lane_on = live && 8 * sub < a.d;
+  const uint32_t per_token = nq + nk + nv;
+  const uint32_t items = (uint32_t)(a.tokens * per_token);  // (below 2^27: checked by the host)
+  const int in_step = 2 * a.d;                              // bytes between rows
 
-  // (the indexes first: loads come back in order, and the angles wait for the position)
-  const int slot_raw = kAppend && live ? __ldg(a.slots + token) : 0;
-  const int pos = live && a.cos_sin ? __ldg(a.positions + token) : 0;
-  int left = live ? in.heads - head0 : 0;  // rows from here on
-  const int in_step = 2 * a.d;             // bytes between rows
-  const uint8_t* src = reinterpret_cast<const uint8_t*>(in.x + token * in.stride + (int64_t)head0 * a.d + 8 * sub);
-  auto load_rows = [&](RowVec (&r)[kRows], int first) {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      r[i] = load_row(reinterpret_cast<const __nv_bfloat16*>(src + (first + i) * in_step), lane_on && first + i < left);
+  // an item: its token, its kind (0 q, 1 k, 2 v) and heads, and what is loaded ahead for it
+  struct Item {
+    int64_t token;
+    const uint8_t* src;
+    int kind, head0, left, pos, slot;  // left: rows from here on
   };
+  auto heads_of = [&](int kind) { return kind == 0 ? a.q.heads : kind == 1 ? a.k.heads : a.v.heads; };
+  auto begin = [&](uint32_t n) {
+    Item t;
+    const bool on = n < items;
+    t.token = on ? n / per_token : 0;
+    const int part = (int)(on ? n % per_token : 0);
+    t.kind = part < nq ? 0 : part < nq + nk ? 1 : 2;
+    t.head0 = (part - (t.kind == 0 ? 0 : t.kind == 1 ? nq : nq + nk)) * rows;
+    t.left = on ? min(heads_of(t.kind) - t.head0, rows) : 0;
+    const __nv_bfloat16* x = t.kind == 0 ? a.q.x : t.kind == 1 ? a.k.x : a.v.x;
+    const int64_t stride = t.kind == 0 ? a.q.stride : t.kind == 1 ? a.k.stride : a.v.stride;
+    t.src = reinterpret_cast<const uint8_t*>(x + t.token * stride + (int64_t)t.head0 * a.d + 8 * sub);
+    // (the indexes before the rows: loads come back in order, and the angles wait for the position)
+    t.slot = kAppend && on ? __ldg(a.slots + t.token) : 0;
+    t.pos = on && a.cos_sin ? __ldg(a.positions + t.token) : 0;
+    return t;
+  };
+  const bool dim_on = 8 * sub < a.d;
+  auto load_rows = [&](RowVec (&r)[kRows], const uint8_t* src, int left) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) r[i] = load_row(reinterpret_cast<const __nv_bfloat16*>(src + i * in_step), dim_on && i < left);
+  };
+  constexpr uint32_t kGroups = kRopeThreads / kLanes;
   RowVec raw[kRows], more[kRows];
-  load_rows(raw, 0);
-  // (the turns of the warp's group with the most: every lane takes part in every exchange)
-  left = min(left, rows);
-  int turns = (left + kRows - 1) / kRows;
-  turns = max(turns, __shfl_xor_sync(0xffffffffu, turns, 16));
-  if (kLanes == 8) turns = max(turns, __shfl_xor_sync(0xffffffffu, turns, 8));
-  int slot = slot_raw;
-  if (kAppend && live) {
-    if (slot >= a.num_slots) {
-      if (a.status) atomicOr(a.status, kStatusBadIndex);
-      slot = -1;
-    }
-    live = slot >= 0;
-  }
-  const float* angles_row = nullptr;
-  if (live && a.cos_sin) {
-    if (pos < 0 || pos >= a.max_pos) {
-      if (a.status) atomicOr(a.status, kStatusBadIndex);
-      live = false;
-    } else {
-      angles_row = a.cos_sin + (int64_t)pos * a.rot;
-    }
-  }
-  const bool norm = in.w != nullptr;
-  Angles ang;
-  load_angles<kLanes, false>(ang, kind == 2 ? nullptr : angles_row, a.rot, a.interleaved, in.w, lane_on);
-
-  // where the rows go, and the bytes between them
-  const bool to_cache = kAppend && kind != 0;
-  uint8_t* dst;
-  float* scale_at = nullptr;
-  int out_step = in_step;
-  if (!to_cache) {
-    __nv_bfloat16* out = kind == 0 ? a.q_out : a.k_out;
-    dst = reinterpret_cast<uint8_t*>(out + (token * in.heads + head0) * a.d + 8 * sub);
-  } else {
-    constexpr int kBytes = kQuant ? 1 : 2;
-    const int64_t page = slot >> a.page_shift;
-    const int64_t line = ((int64_t)head0 << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
-    const int64_t at = page * (kind == 1 ? a.k_page_stride : a.v_page_stride) + line * a.d + 8 * sub;
-    dst = static_cast<uint8_t*>(kind == 1 ? a.k_cache : a.v_cache) + at * kBytes;
-    out_step = (a.d * kBytes) << a.page_shift;
-    if (kQuant) scale_at = (kind == 1 ? a.k_scale : a.v_scale) + ((page * in.heads) << a.page_shift) + line;
-  }
-  const float inv_d = 1.f / (float)a.d;
-  const bool write = live && lane_on;
-
-  auto work = [&](const RowVec (&cur)[kRows], RowVec (&next)[kRows]) {
-    load_rows(next, kRows);
-    float ss[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const Row8 x = to_float(cur[i]);
-      F2 t = mul2(x.v[0], x.v[0]);
-#pragma unroll
-      for (int j = 1; j < 4; ++j) t = fma2(x.v[j], x.v[j], t);
-      const float2 u = un2(t);
-      ss[i] = u.x + u.y;
-    }
-    const float total = sum4<kLanes>(ss);
-    const float rr = norm ? rsqrtf(total * inv_d + a.eps) : 1.f;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float r = __shfl_sync(0xffffffffu, rr, sum4_lane<kLanes>(i));
-      Row8 x = rotated(to_float(cur[i]), paired(cur[i], ang, a.interleaved), ang);
-      const F2 r2 = f2(r, r);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], r2);
-      const bool on = write && i < left;
-      uint32_t big = 0;
-      if (kQuant) {
-        // the largest magnitude by its bits: an infinity or NaN is larger than every number
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 t = un2(x.v[j]);
-          big = max(big, max(__float_as_uint(t.x) & 0x7fffffffu, __float_as_uint(t.y) & 0x7fffffffu));
-        }
-        big = group_max<kLanes>(big);
-      }
-      if (!on) continue;
-      if (kQuant && to_cache) {
-        const float scale = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : fmaxf(__fdiv_rn(__uint_as_float(big), kE4M3Max), kKvScaleFloor);
-        *reinterpret_cast<uint2*>(dst + i * out_step) = e4m3_codes(x, scale);
-        if (sub == 0) scale_at[i << a.page_shift] = scale;
-      } else {
-        // (values go to a bf16 cache as they are)
-        *reinterpret_cast<uint4*>(dst + i * out_step) =
-            kAppend && !kQuant && kind == 2 ? make_uint4(cur[i].u[0], cur[i].u[1], cur[i].u[2], cur[i].u[3]) : to_bf16(x);
-      }
-    }
-    left -= kRows;
-    src += kRows * in_step;
-    dst += kRows * out_step;
-    if (kQuant) scale_at += (int64_t)kRows << a.page_shift;
-  };
+  Item now = begin(blockIdx.x * kGroups + threadIdx.x / kLanes);
+  load_rows(raw, now.src, now.left);
 #pragma unroll 1
-  for (int turn = 0; turn < turns; turn += 2) {
-    work(raw, more);
-    if (turn + 1 < turns) work(more, raw);
+  for (uint32_t first = blockIdx.x * kGroups; first < items; first += gridDim.x * kGroups) {
+    Item after = {};
+    if (kLoop) after = begin(first + gridDim.x * kGroups + threadIdx.x / kLanes);
+    const int64_t token = now.token;
+    const int kind = now.kind, head0 = now.head0, pos = now.pos;
+    int left = now.left, slot = now.slot;
+    const uint8_t* src = now.src;
+    bool live = left > 0;  // (every lane stays for the shuffles)
+    const int heads = heads_of(kind);
+    const float* weight = kind == 0 ? a.q.w : kind == 1 ? a.k.w : nullptr;
+    // (the turns of the warp's group with the most: every lane takes part in every exchange)
+    int turns = (left + kRows - 1) / kRows;
+    turns = max(turns, __shfl_xor_sync(0xffffffffu, turns, 16));
+    if (kLanes == 8) turns = max(turns, __shfl_xor_sync(0xffffffffu, turns, 8));
+    if (kAppend && live) {
+      if (slot >= a.num_slots) {
+        if (a.status) atomicOr(a.status, kStatusBadIndex);
+        slot = -1;
+      }
+      live = slot >= 0;
+    }
+    const float* angles_row = nullptr;
+    if (live && a.cos_sin) {
+      if (pos < 0 || pos >= a.max_pos) {
+        if (a.status) atomicOr(a.status, kStatusBadIndex);
+        live = false;
+      } else {
+        angles_row = a.cos_sin + (int64_t)pos * a.rot;
+      }
+    }
+    const bool norm = weight != nullptr;
+    Angles ang;
+    load_angles<kLanes, false>(ang, kind == 2 ? nullptr : angles_row, a.rot, a.interleaved, weight, dim_on);
+
+    // where the rows go, and the bytes between them
+    const bool to_cache = kAppend && kind != 0;
+    uint8_t* dst;
+    float* scale_at = nullptr;
+    int out_step = in_step;
+    if (!to_cache) {
+      __nv_bfloat16* out = kind == 0 ? a.q_out : a.k_out;
+      dst = reinterpret_cast<uint8_t*>(out + (token * heads + head0) * a.d + 8 * sub);
+    } else {
+      constexpr int kBytes = kQuant ? 1 : 2;
+      const int64_t page = slot >> a.page_shift;
+      const int64_t line = ((int64_t)head0 << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
+      const int64_t at = page * (kind == 1 ? a.k_page_stride : a.v_page_stride) + line * a.d + 8 * sub;
+      dst = static_cast<uint8_t*>(kind == 1 ? a.k_cache : a.v_cache) + at * kBytes;
+      out_step = (a.d * kBytes) << a.page_shift;
+      if (kQuant) scale_at = (kind == 1 ? a.k_scale : a.v_scale) + ((page * heads) << a.page_shift) + line;
+    }
+    const float inv_d = 1.f / (float)a.d;
+    const bool write = live && dim_on;
+
+    auto work = [&](const RowVec (&cur)[kRows], RowVec (&next)[kRows], bool last) {
+      load_rows(next, last ? after.src : src + kRows * in_step, last ? after.left : left - kRows);
+      float ss[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const Row8 x = to_float(cur[i]);
+        F2 t = mul2(x.v[0], x.v[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) t = fma2(x.v[j], x.v[j], t);
+        const float2 u = un2(t);
+        ss[i] = u.x + u.y;
+      }
+      const float total = sum4<kLanes>(ss);
+      const float rr = norm ? rsqrtf(total * inv_d + a.eps) : 1.f;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float r = __shfl_sync(0xffffffffu, rr, sum4_lane<kLanes>(i));
+        Row8 x = rotated(to_float(cur[i]), paired(cur[i], ang, a.interleaved), ang);
+        const F2 r2 = f2(r, r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], r2);
+        const bool on = write && i < left;
+        uint32_t big = 0;
+        if (kQuant) {
+          // the largest magnitude by its bits: an infinity or NaN is larger than every number
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 t = un2(x.v[j]);
+            big = max(big, max(__float_as_uint(t.x) & 0x7fffffffu, __float_as_uint(t.y) & 0x7fffffffu));
+          }
+          big = group_max<kLanes>(big);
+        }
+        if (!on) continue;
+        if (kQuant && to_cache) {
+          const float scale = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : fmaxf(__fdiv_rn(__uint_as_float(big), kE4M3Max), kKvScaleFloor);
+          *reinterpret_cast<uint2*>(dst + i * out_step) = e4m3_codes(x, scale);
+          if (sub == 0) scale_at[i << a.page_shift] = scale;
+        } else {
+          // (values go to a bf16 cache as they are)
+          *reinterpret_cast<uint4*>(dst + i * out_step) =
+              kAppend && !kQuant && kind == 2 ? make_uint4(cur[i].u[0], cur[i].u[1], cur[i].u[2], cur[i].u[3]) : to_bf16(x);
+        }
+      }
+      left -= kRows;
+      src += kRows * in_step;
+      dst += kRows * out_step;
+      if (kQuant) scale_at += (int64_t)kRows << a.page_shift;
+    };
+#pragma unroll 1
+    for (int turn = 0; turn < turns; turn += 2) {
+      work(raw, more, turn + 1 >= turns);
+      if (turn + 1 < turns) {
+        work(more, raw, turn + 2 >= turns);
+      } else if (kLoop) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) raw[i] = more[i];
+      }
+    }
+    if (!kLoop) break;
+    now = after;
   }
 }
 
@@ -557,18 +587,22 @@ template <int kLanes>
 cudaError_t launch_rope(const RopeArgs& a, bool append, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  // As many rows per group as leave every SM eight blocks or more, and few turns empty (heads that do
-  // not fill their groups): at 32 + 8 + 8 heads 4097 tokens take 30 us with 8 rows and 41 us with 32,
-  // at 96 + 12 heads 32768 tokens take 537 us with 4 rows, 394 with 8, 337 with 16.
+  // As many rows per group as leave the device full, and few turns empty (heads that do
+  // not fill their groups): at 32 + 8 + 8 heads 4097 tokens take 29 us with 4 rows and 24 with 8 or 16,
+  // 256 tokens (e4m3) 5.7 us with 4 and 7.9 with 8; at 96 + 12 heads 32768 tokens take 399 us with 4 rows,
+  // 314 with 8, 293 with 16 or 32.
   auto items = [&](int b) { return rope_items(1, a.q.heads, a.k.heads, a.v.heads, b); };
   auto blocks = [&](int b) { return (a.tokens * items(b) * kLanes + kRopeThreads - 1) / kRopeThreads; };
   int batches = 1;
-  while (batches < 8 && blocks(2 * batches) >= 8 * (int64_t)sms && items(2 * batches) * 2 * batches * 8 <= items(1) * 9) batches *= 2;
-  const int64_t grid = blocks(batches);
-  if (grid == 0) return cudaSuccess;
-  if (!append) norm_rope_kernel<kLanes, false, false><<<(unsigned)grid, kRopeThreads, 0, stream>>>(a, batches);
-  else if (a.k_scale) norm_rope_kernel<kLanes, true, true><<<(unsigned)grid, kRopeThreads, 0, stream>>>(a, batches);
-  else norm_rope_kernel<kLanes, true, false><<<(unsigned)grid, kRopeThreads, 0, stream>>>(a, batches);
+  while (batches < 8 && blocks(2 * batches) >= kRopeCtas * (int64_t)sms && items(2 * batches) * 2 * batches * 8 <= items(1) * 9) batches *= 2;
+  const int64_t all = blocks(batches), resident = (int64_t)kRopeCtas * sms;
+  if (all == 0) return cudaSuccess;
+  const bool loop = all > resident;
+  auto kernel = loop ? (!append ? norm_rope_kernel<kLanes, false, false, true> : a.k_scale ? norm_rope_kernel<kLanes, true, true, true>
+                                                                                            : norm_rope_kernel<kLanes, true, false, true>)
+                     : (!append ? norm_rope_kernel<kLanes, false, false, false> : a.k_scale ? norm_rope_kernel<kLanes, true, true, false>
+                                                                                             : norm_rope_kernel<kLanes, true, false, false>);
+  kernel<<<(unsigned)(loop ? resident : all), kRopeThreads, 0, stream>>>(a, batches);
   return cudaGetLastError();
 }
 

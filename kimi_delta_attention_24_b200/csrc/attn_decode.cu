@@ -15,15 +15,15 @@
 //   - Each of a CTA's warps streams its own tiles (one per block) through its own ring of stages, with
 //     no CTA barrier: 16-byte cp.async copies into swizzled rows (conflict-free matrix loads), under way
 //     also across the ends of units; about 130 KB of copies in flight per SM.  (TMA boxes instead cost
-//     the issuing warp 800 to 900 cycles a tile, four boxes each, of 2600 to 3400.)
+//     the issuing warp 800 to 900 cycles a tile, four boxes each, of 2600 to 3500.)
 //   - The warps' results of a unit meet as a chain through shared memory, so that no warp waits for a
 //     slower one before it goes on with the next unit.  With very many units each warp takes a share of
 //     its own instead; few short units are not split at all.
 //   - The products are transposed, S^T = K Q^T and O^T = V^T P^T, mma.sync m16n8k16 with the keys (the
 //     channels) as the 16 and 8 rows of queries as the 8: a unit of up to 8 rows (one kv head's group
 //     at T = 1) wastes half as much of each instruction, and half the registers, as with 16 rows.
-//   - What remains to be hidden is latency: two warps per scheduler took 2600 to 3400 cycles a tile
-//     whether its bytes had arrived or not.  So dependent products are kept apart, and the softmax
+//   - What remains to be hidden is latency: two warps per scheduler take 2600 to 3500 cycles a tile
+//     whether its bytes have arrived or not.  So dependent products are kept apart, and the softmax
 //     exchanges maxima between threads only when a score passes its row's reference by 2^8.
 //   - bf16 cache: P enters the second product as a bf16 pair hi + lo, so its rounding (2^-17) stays
 //     below that of the bf16 output.  e4m3 cache: codes are exact in fp16; the key's scale multiplies
@@ -31,6 +31,8 @@
 //     reference of that sum (within 2^8 of its maximum), whatever the scales are; times 2^7 it is rounded
 //     to fp16 (2^-11 down to 2^-21 of 2^M).  q (bf16) is scaled by a power of two per row to fit fp16.
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "attn_common.cuh"
 #include "kda_device.cuh"
@@ -221,14 +223,14 @@ template <bool kFp8, int kDP, int kNQ, Mode kMode>
 struct Smem {
   using G = Geo<kFp8, kDP, kNQ, kMode>;
   static constexpr int kWarps = G::kWarps;
-  static constexpr int kQPlaces = kMode == kSolo ? 2 * kWarps : 3;                             // two of each warp, or three of all
+  static constexpr int kQPlaces = kMode == kSolo ? 2 * kWarps : 3;  // two of each warp, or three of all
   static constexpr int kRows = 8 * kNQ, kDM = kDP / 16;
-  static constexpr int kQRowBytes = kRows * kDP * 2;                                  // one unit's queries as they are
-  static constexpr int kScaleOff = kWarps * G::kWarpBytes;                         // (the rings come first)
+  static constexpr int kQRowBytes = kRows * kDP * 2;                // one unit's queries as they are
+  static constexpr int kScaleOff = kWarps * G::kWarpBytes;          // (the rings come first)
   static constexpr int kQOff = kScaleOff + kWarps * G::kStages * G::kScaleBytes;
-  static constexpr int kSumOff = kQOff + kQPlaces * kQRowBytes;            // the warps' sum,
-  static constexpr int kMlOff = kSumOff + (kMode == kSolo ? 0 : kNQ * kDM * 32 * 16);          // and each row's maximum and sum
-  static constexpr int kScanOff = kMlOff + (kMode == kSolo ? 0 : kNQ * 32 * 16);                             // one int64 per warp
+  static constexpr int kSumOff = kQOff + kQPlaces * kQRowBytes;         // the warps' sum,
+  static constexpr int kMlOff = kSumOff + (kMode == kSolo ? 0 : kNQ * kDM * 32 * 16);  // and each row's maximum and sum
+  static constexpr int kScanOff = kMlOff + (kMode == kSolo ? 0 : kNQ * 32 * 16);       // one int64 per warp
   static constexpr int kTotal = kScanOff + 8 * kWarps;
 };
 
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
       const uint32_t st = ring + stage_in * G::kStageBytes;
       if (in_first) {
         // the unit's queries come with its first tile: a load that is waited for at the unit's start
-        // would queue behind all the copies under way.  All four warps of a shared unit copy them (the
+        // would queue behind all the copies under way.  All warps of a shared unit copy them (the
         // same bytes); of three places the one behind a warp that lags and before one that leads is free.
         in_first = false;
         constexpr int kQChunks = kDP * 2 / 16, kQPass = 32 / kQChunks;
@@ -1231,7 +1233,7 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
 // then, but a unit is one warp's work.  (128 sequences, 8 kv heads, bf16: 80 rows, 5120 units, take 154 us
 // in common and 78 alone at 120 keys, 473 and 442 at 2000; 16 rows, 1024 units, take 35 and 41, 105 and 124.)
 constexpr int64_t kSoloUnits = 4;
-// Keys in the tables up to which units that all find an SM are not split: one launch, no join, but a
+// Keys in the tables (or the window) up to which units that all find an SM are not split: one launch, no join, but a
 // unit is one CTA's work.  The more units there are, the less splitting them helps; lengths that differ
 // are what the second bound is for.  (bf16, 4 rows of 128 channels, split and whole: 8 units take 9.8 and
 // 7.3 us at 333 keys, 10.1 and 10.1 at 760, 11.1 and 15.2 at 1500; 128 units 13.8 and 8.0, 16.9 and 10.8, 18.3 and
@@ -1243,7 +1245,8 @@ cudaError_t launch_mode(const AttnDecodeArgs& a, int64_t units, cudaStream_t str
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   if (units >= kSoloUnits * Geo<kFp8, kDP, kNQ, kCommon>::kWarps * kCtasPerSm * sms) return launch_typed<kFp8, kDP, kNQ, kSolo>(a, stream);
-  const int64_t keys = (int64_t)a.max_pages << a.page_shift;
+  int64_t keys = (int64_t)a.max_pages << a.page_shift;  // the most that a unit can have
+  if (a.window > 0) keys = std::min<int64_t>(keys, (int64_t)a.window + a.new_tokens - 1);
   if (units <= sms && keys <= kWholeMost && keys * (sms - units) <= kWholeKeys * sms)
     return launch_typed<kFp8, kDP, kNQ, kWhole>(a, stream);
   return launch_typed<kFp8, kDP, kNQ, kCommon>(a, stream);
