@@ -47,6 +47,10 @@ ROPE = [
     (64, 8, 2, 112, 0, False, True, True),
     (17, 6, 6, 48, 16, False, False, False),
     (300, 13, 7, 128, 64, False, True, True),
+    # more items than a full device takes at once: one head group per item, and several
+    (5003, 5, 1, 128, 64, True, True, True),
+    (1601, 64, 16, 96, 96, False, True, True),
+    (9001, 3, 1, 48, 32, False, True, True),
 ]
 
 
@@ -162,7 +166,8 @@ def test_norm_rope_bwd_against_differences():
 # ------------------------------------------------------------------------------------ the cache
 @pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("case,page", [(ROPE[0], 8), (ROPE[1], 16), (ROPE[2], 64), (ROPE[3], 32), (ROPE[4], 16), (ROPE[6], 128),
-                                       (ROPE[7], 8), (ROPE[8], 1024), (ROPE[9], 16)], ids=lambda c: str(c).replace(" ", ""))
+                                       (ROPE[7], 8), (ROPE[8], 1024), (ROPE[9], 16),
+                                       (ROPE[10], 16), (ROPE[11], 64), (ROPE[12], 8)], ids=lambda c: str(c).replace(" ", ""))
 def test_append(cuda_device, case, page, quant):
     tokens, hq, hk, d, rot, inter, *_ = case
     qkv, wq, wk, tab, pos = rope_inputs(case, 6)
