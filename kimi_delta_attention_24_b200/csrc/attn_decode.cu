@@ -9,7 +9,7 @@
 // head, T new tokens), 4 G T flops per 2 x 2 bytes (bf16): HBM, until G T is near 64.  So the design
 // is a stream of cache tiles with little else:
 //   - Split: the (sequence, kv head, row block) units are laid end to end as blocks of one tile of keys
-//     per warp, and every CTA (two per SM) takes an equal share of all blocks, wherever it
+//     per warp, and every CTA (two or three per SM) takes an equal share of all blocks, wherever it
 //     begins and ends, so ragged lengths cost no balance.  A unit that several CTAs share leaves fp32
 //     partial results (o, m, l) in the workspace, joined in a fixed order by a second, dependent launch.
 //   - Each of a CTA's warps streams its own tiles (one per block) through its own ring of stages, with
@@ -22,7 +22,7 @@
 //   - The products are transposed, S^T = K Q^T and O^T = V^T P^T, mma.sync m16n8k16 with the keys (the
 //     channels) as the 16 and 8 rows of queries as the 8: a unit of up to 8 rows (one kv head's group
 //     at T = 1) wastes half as much of each instruction, and half the registers, as with 16 rows.
-//   - What remains to be hidden is latency: two warps per scheduler take 2600 to 3500 cycles a tile
+//   - What remains to be hidden is latency: two or three warps per scheduler take 2600 to 3500 cycles a tile
 //     whether its bytes have arrived or not.  So dependent products are kept apart, and the softmax
 //     exchanges maxima between threads only when a score passes its row's reference by 2^8.
 //   - bf16 cache: P enters the second product as a bf16 pair hi + lo, so its rounding (2^-17) stays
@@ -44,9 +44,8 @@ namespace {
 // units are very many (kSolo); or each unit to one CTA, where they are few and short (kWhole).
 enum Mode { kCommon, kSolo, kWhole };
 
-constexpr int kCtasPerSm = 2;               // (kWhole: one of twice the warps)
-constexpr int kMaxCtas = kCtasPerSm * 160;  // bound used for the workspace (148 SMs on a B200)
-constexpr int kMaxShares = kMaxCtas * 4;    // (kSolo)
+constexpr int kMaxSms = 160;               // bound used for the workspace (148 on a B200)
+constexpr int kMaxShares = kMaxSms * 2 * 4;  // (kSolo)
 constexpr float kLazy = 8.0f;         // how far (base 2) a score passes a row's reference before it moves
 constexpr float kWeightShift = 7.0f;  // fp16 weights: up to 2^(kLazy + kWeightShift) = 2^15
 
@@ -129,19 +128,23 @@ __device__ __forceinline__ float tanh_any(float x) {
 // Tile geometry.  kDP: the head size padded to 64 or 128 channels (the padding is zero in q and in
 // the loaded rows); kNQ: tiles of 8 rows per unit (1 or 2); kTok: keys of one warp's tile, 8 KB of K and V
 // together (4 KB for 64 e4m3 channels); a block is one tile per warp.  Two CTAs of 4 warps per SM:
-// their registers allow no more beyond 8 rows; up to 8, more warps (two CTAs of 6, three of 4) were no
-// faster for long sequences and slower for short ones.  The bf16 cache has room for a third stage there.
+// at 128 channels their registers allow no more beyond 8 rows; up to 8, more warps (two CTAs of 6, three of
+// 4) were no faster for long sequences and slower for short ones.  The bf16 cache has room for a third stage
+// there, and needs the stages more than a third CTA at 64 channels (4 rows: 51.1 us with two, 51.6 with three).
 template <bool kFp8, int kDP, int kNQ, Mode kMode>
 struct Geo {
   static constexpr int kWarps = kMode == kWhole ? 8 : 4;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCtas = kMode == kWhole ? 1 : kCtasPerSm;   // per SM
+  // CTAs per SM: three at 64 e4m3 channels, whose tiles are small (64 sequences to 4096: 4 rows of 8 kv heads
+  // 43.0 us with two and 38.9 with three, 12 rows of 4 heads 35.1 and 33.2)
+  static constexpr int kCtas = kMode == kWhole ? 1 : kMode == kCommon && kDP == 64 && kFp8 ? 3 : 2;
+  static constexpr int kMaxCtas = kMaxSms * kCtas;
   static constexpr int kTok = kFp8 ? 32 : (kDP == 128 ? 16 : 32);
   static constexpr int kRowBytes = kFp8 ? kDP : 128;               // bytes of a row in one column block
   static constexpr int kColBlocks = kFp8 ? 1 : kDP / 64;           // 128-byte column blocks (bf16)
   static constexpr int kOpBytes = kTok * kRowBytes * kColBlocks;   // K (or V) of one tile
   static constexpr int kStageBytes = 2 * kOpBytes;
-  static constexpr int kWarpBytes = kNQ == 1 && !kFp8 ? 24576 : 16384;
+  static constexpr int kWarpBytes = kCtas == 3 ? 12288 : kNQ == 1 && !kFp8 ? 24576 : 16384;
   static constexpr int kStages = kWarpBytes / kStageBytes;
   static constexpr int kShares = kMode == kSolo ? kWarps : 1;      // shares of a CTA
   static constexpr int kBlockTok = kTok * (kMode == kSolo ? 1 : kWarps);
@@ -1002,14 +1005,16 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
 // Joins the partial results of every unit that more than one share has a part of, in the order of its
 // keys; fp32 sums.  The launch's blocks take jobs in turn: a row tile, its channel tiles a warp each, where a unit
 // has few partials; a row tile's one channel tile, the partials dealt to the eight warps, where it
-// has many.
+// has many.  (It does not release the launch after it early: CTAs of a next main kernel that are placed
+// beside this one's lie unevenly over the SMs.  48 sequences to 8192, three CTAs per SM: 42.4 us a call
+// in a row, against 33.4.)
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kFewPartials = 8;
 
 template <bool kFp8, int kDP, int kNQ, Mode kMode>
 __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid_constant__ DecodeParams p, int grid) {
   using G = Geo<kFp8, kDP, kNQ, kMode>;
-  constexpr int kDM = kDP / 16, kMost = kMaxCtas * G::kShares, kPer = (kMost + kJoinThreads - 1) / kJoinThreads;
+  constexpr int kDM = kDP / 16, kMost = G::kMaxCtas * G::kShares, kPer = (kMost + kJoinThreads - 1) / kJoinThreads;
   const AttnDecodeArgs& a = p.a;
   __shared__ int s_end[kMost];    // jobs up to and with the unit that share i ends
   __shared__ int4 s_meta[kMost];  // that unit: first partial, partials, unit
@@ -1017,7 +1022,6 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
   __shared__ int64_t s_sum[kJoinThreads];
   __shared__ float4 s_o[kJoinWarps][32], s_ml[kJoinWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  sm100::griddep_launch_dependents();
 
   // Who worked on what follows from the lengths, as in the main kernel (which has begun, so what wrote
   // them is done): found before the wait for its results.
@@ -1199,8 +1203,8 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   const int64_t units = (int64_t)a.batch * a.hkv * p.row_blocks;
   const int64_t cap = (int64_t)a.max_pages << a.page_shift;
   const int64_t most_blocks = cap > G::kBlockTok ? (cap + G::kBlockTok - 1) / G::kBlockTok : 1;
-  int64_t grid = (int64_t)kCtasPerSm * sms;
-  if (grid > kMaxCtas) grid = kMaxCtas;
+  int64_t grid = (int64_t)G::kCtas * sms;
+  if (grid > G::kMaxCtas) grid = G::kMaxCtas;
   const int64_t most_shares = units < grid * G::kWarps ? units * (most_blocks + kUnitCost) : INT64_MAX;
   if (most_shares < grid * G::kShares) grid = (most_shares + G::kShares - 1) / G::kShares;
   if (kMode == kWhole) grid = units;
@@ -1244,7 +1248,7 @@ template <bool kFp8, int kDP, int kNQ>
 cudaError_t launch_mode(const AttnDecodeArgs& a, int64_t units, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  if (units >= kSoloUnits * Geo<kFp8, kDP, kNQ, kCommon>::kWarps * kCtasPerSm * sms) return launch_typed<kFp8, kDP, kNQ, kSolo>(a, stream);
+  if (units >= kSoloUnits * Geo<kFp8, kDP, kNQ, kSolo>::kWarps * Geo<kFp8, kDP, kNQ, kSolo>::kCtas * sms) return launch_typed<kFp8, kDP, kNQ, kSolo>(a, stream);
   int64_t keys = (int64_t)a.max_pages << a.page_shift;  // the most that a unit can have
   if (a.window > 0) keys = std::min<int64_t>(keys, (int64_t)a.window + a.new_tokens - 1);
   if (units <= sms && keys <= kWholeMost && keys * (sms - units) <= kWholeKeys * sms)
