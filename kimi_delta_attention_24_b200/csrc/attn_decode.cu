@@ -163,8 +163,7 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 }
 
 // Keys [lo, hi) that any row of a sequence sees.
-__device__ __forceinline__ void key_range(const AttnDecodeArgs& a, int b, int& lo, int& hi, uint32_t* status) {
-  int len = a.seq_lens[b];
+__device__ __forceinline__ void key_range(const AttnDecodeArgs& a, int len, int& lo, int& hi, uint32_t* status) {
   const int64_t cap = (int64_t)a.max_pages << a.page_shift;
   if (len < 0 || len > cap) {
     if (status) atomicOr(status, kStatusBadIndex);
@@ -187,28 +186,40 @@ __device__ __forceinline__ int num_blocks(int lo, int hi) {
 constexpr int kUnitCost = 3;
 
 // A CTA's share of all units' blocks, piece by piece: next() steps to the blocks [blk, blk + take) of
-// the next unit, until the share is used up.
+// the next unit, until the share is used up.  lens: the lengths in shared memory, or null where there are
+// more than kLens (a load from global memory waits behind all the copies under way).
+constexpr int kLens = 512;
 template <int kBlockTok>
 struct Walk {
-  int64_t left, off;  // cost left in the share; position of its cursor in sequence next_b
-  int next_b;
-  int b, u, lo, len, n_blk, blk, take;  // the piece
-  __device__ __forceinline__ bool next(const AttnDecodeArgs& a, int64_t units_per_seq) {
+  int64_t left;                          // cost left in the share
+  int b, u, lo, len, n_blk, blk, take;   // the piece
+  int pos;                               // the cursor behind it, in the unit's cost (its blocks come first)
+  __device__ __forceinline__ void to_sequence(const AttnDecodeArgs& a, const int* lens) {
+    key_range(a, lens ? lens[b] : a.seq_lens[b], lo, len, nullptr);
+    n_blk = num_blocks<kBlockTok>(lo, len);
+  }
+  // To position `off` of sequence `first`.
+  __device__ __forceinline__ void begin(const AttnDecodeArgs& a, const int* lens, int first, int64_t off) {
+    b = first;
+    to_sequence(a, lens);
+    u = (int)divide(off, n_blk + kUnitCost);
+    pos = (int)(off - (int64_t)u * (n_blk + kUnitCost));
+  }
+  __device__ __forceinline__ bool next(const AttnDecodeArgs& a, const int* lens, int64_t units_per_seq) {
     while (left > 0) {
-      b = next_b;
-      key_range(a, b, lo, len, nullptr);
-      n_blk = num_blocks<kBlockTok>(lo, len);
-      const int n_cost = n_blk + kUnitCost;
-      u = (int)divide(off, n_cost);
-      blk = (int)(off - (int64_t)u * n_cost);
-      const int step = (int)min((int64_t)(n_cost - blk), left);  // of the unit's cost; its blocks come first
+      if (pos == n_blk + kUnitCost) {
+        pos = 0;
+        if (++u == units_per_seq) {
+          u = 0;
+          ++b;
+          to_sequence(a, lens);
+        }
+      }
+      blk = pos;
+      const int step = (int)min((int64_t)(n_blk + kUnitCost - blk), left);
       take = min(n_blk - blk, step);
       left -= step;
-      off += step;
-      if (off == n_cost * units_per_seq) {
-        ++next_b;
-        off = 0;
-      }
+      pos += step;
       if (take > 0) return true;
     }
     return false;
@@ -273,6 +284,8 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
   int64_t* s_scan = reinterpret_cast<int64_t*>(smem + SM::kScanOff);
   __shared__ int s_b[G::kShares];
   __shared__ int64_t s_off[G::kShares];
+  __shared__ int s_len[kMode == kWhole ? 1 : kLens];
+  const int* lens = kMode != kWhole && a.batch <= kLens ? s_len : nullptr;
 
   // (this launch may begin while the one before it drains, and the join while this one does: each
   // waits here for all that ran before)
@@ -287,13 +300,11 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
     if (blockIdx.x == 0)
       for (int b = tid; b < a.batch; b += kThreads) {
         int lo, hi;
-        key_range(a, b, lo, hi, p.status);
+        key_range(a, a.seq_lens[b], lo, hi, p.status);
       }
-    in.next_b = (int)(share / units_per_seq);
-    int lo, hi;
-    key_range(a, in.next_b, lo, hi, nullptr);
-    in.left = num_blocks<G::kBlockTok>(lo, hi);
-    in.off = (share - in.next_b * units_per_seq) * (in.left + kUnitCost);
+    in.begin(a, nullptr, (int)(share / units_per_seq), 0);
+    in.u = (int)(share - in.b * units_per_seq);
+    in.left = in.n_blk;
     if (tid == 0) s_any = 0;
     __syncthreads();
   } else {
@@ -303,7 +314,9 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
     int64_t mine = 0;
     for (int b = b_first; b < b_last; ++b) {
       int lo, hi;
-      key_range(a, b, lo, hi, blockIdx.x == 0 ? p.status : nullptr);
+      const int len = a.seq_lens[b];
+      if (b < kLens) s_len[b] = len;
+      key_range(a, len, lo, hi, blockIdx.x == 0 ? p.status : nullptr);
       mine += (num_blocks<G::kBlockTok>(lo, hi) + kUnitCost) * units_per_seq;
     }
     int64_t incl = mine;
@@ -328,7 +341,7 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
         int64_t at = before;
         for (int b = b_first; b < b_last; ++b) {
           int lo, hi;
-          key_range(a, b, lo, hi, nullptr);
+          key_range(a, lens ? lens[b] : a.seq_lens[b], lo, hi, nullptr);
           const int64_t n = (num_blocks<G::kBlockTok>(lo, hi) + kUnitCost) * units_per_seq;
           if (first < at + n) {
             s_b[k] = b;
@@ -343,8 +356,7 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
     share = (int64_t)blockIdx.x * G::kShares + (kMode == kSolo ? warp : 0);
     if (share >= shares) return;
     in.left = divide((share + 1) * total, shares) - divide(share * total, shares);
-    in.off = s_off[kMode == kSolo ? warp : 0];
-    in.next_b = s_b[kMode == kSolo ? warp : 0];
+    in.begin(a, lens, s_b[kMode == kSolo ? warp : 0], s_off[kMode == kSolo ? warp : 0]);
   }
   out = in;
 
@@ -380,7 +392,7 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
     ++in_i;
     bool fresh = !one_page || in_i - in_batch == 32;
     while (in_i >= in_end) {
-      in_more = in.next(a, units_per_seq);
+      in_more = in.next(a, lens, units_per_seq);
       if (!in_more) return;
       ++in_piece;
       in_slot = in_slot == kPlaces - 1 ? 0 : in_slot + 1;
@@ -467,13 +479,13 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
   advance();
 
   int pieces = 0, slot_out = 0;
-  bool more = out.next(a, units_per_seq);
+  bool more = out.next(a, lens, units_per_seq);
   while (more) {
     const int b = out.b, len = out.len, lo = out.lo, blk = out.blk, take = out.take, n_blk = out.n_blk, u = out.u;
     const int h = u / p.row_blocks, row_base = (u - h * p.row_blocks) * kRows;
     int tok0, i_begin, i_end;
     out.tiles(kMode == kSolo ? 0 : warp, kTok, tok0, i_begin, i_end);
-    more = out.next(a, units_per_seq);
+    more = out.next(a, lens, units_per_seq);
 
     // ---- the rows' key ranges, their queries as fragments.  A lane works on the scores of rows
     // 2 c + {0, 1} of each row tile, and holds the queries of row g.
@@ -1029,7 +1041,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
   const int per = (a.batch + kJoinThreads - 1) / kJoinThreads;
   auto seq_cost = [&](int b, int& n_blk) {
     int lo, hi;
-    key_range(a, b, lo, hi, nullptr);
+    key_range(a, a.seq_lens[b], lo, hi, nullptr);
     n_blk = num_blocks<G::kBlockTok>(lo, hi);
     return (n_blk + kUnitCost) * units_per_seq;
   };
