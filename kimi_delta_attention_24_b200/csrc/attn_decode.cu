@@ -1246,14 +1246,14 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
 }
 
 // Units per warp from which warps take shares of their own: their results of a unit need no joining
-// then, but a unit is one warp's work.  (128 sequences, 8 kv heads, bf16: 80 rows, 5120 units, take 154 us
-// in common and 78 alone at 120 keys, 473 and 442 at 2000; 16 rows, 1024 units, take 35 and 41, 105 and 124.)
+// then, but a unit is one warp's work.  (128 sequences, 8 kv heads, bf16: 80 rows, 5120 units, take 149 us
+// in common and 77 alone at 120 keys, 466 and 439 at 2000; 16 rows, 1024 units, 35 and 41, 105 and 124.)
 constexpr int64_t kSoloUnits = 4;
-// Keys in the tables (or the window) up to which units that all find an SM are not split: one launch, no join, but a
-// unit is one CTA's work.  The more units there are, the less splitting them helps; lengths that differ
-// are what the second bound is for.  (bf16, 4 rows of 128 channels, split and whole: 8 units take 9.8 and
-// 7.3 us at 333 keys, 10.1 and 10.1 at 760, 11.1 and 15.2 at 1500; 128 units 13.8 and 8.0, 16.9 and 10.8, 18.3 and
-// 15.5.  16 rows, 8 units: 12.5 and 9.8, 11.4 and 12.9.)
+// Keys in the tables (or the window) up to which units that all find an SM are not split: one launch,
+// no join, but a unit is one CTA's work.  The more units there are, the less splitting them helps;
+// lengths that differ are what the second bound is for.  (bf16, 4 rows of 128 channels, split and whole:
+// 8 units take 10.1 and 6.8 us at 333 keys, 10.2 and 9.4 at 760, 11.2 and 14.3 at 1500; 128 units 14.0 and
+// 7.4, 16.9 and 10.1, 18.3 and 14.7.  16 rows, 8 units: 12.7 and 9.4, 11.5 and 13.2.)
 constexpr int64_t kWholeKeys = 640, kWholeMost = 1024;
 
 template <bool kFp8, int kDP, int kNQ>
