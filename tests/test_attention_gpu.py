@@ -501,6 +501,23 @@ def test_decode_many_sequences(cuda_device):
     check_decode(lens, 1, 2, 1, 16, 8, False)
 
 
+@pytest.mark.parametrize("b,hk", [(147, 1), (148, 1), (149, 1), (74, 2), (511, 1), (512, 1), (513, 1), (600, 8)])
+def test_decode_batches_where_the_form_changes(cuda_device, b, hk):
+    """A unit per SM and one more; the lengths that fit shared memory and one more; beyond them with a share per warp."""
+    gen = torch.Generator().manual_seed(b)
+    lens = torch.randint(0, 30, (b,), generator=gen).tolist()
+    lens[b // 3] = 170
+    check_decode(lens, 1, hk, 2, 16, 8, b % 2 == 1)
+
+
+@pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("new,group", [(1, 4), (3, 4), (4, 6)])
+def test_decode_short_window_in_long_sequences(cuda_device, new, group, quant):
+    """Few units with few keys each although the tables are long: not split, from the window's first key on."""
+    check_decode([5000, 1200, 3, 0, 2049], new, 2, group, 128, 16, quant, window=300)
+    check_decode([1300, 4111], new, 1, group, 64, 64, quant, window=33)
+
+
 @pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("d,new,group,window", [(64, 1, 1, 0), (128, 3, 2, 9), (128, 2, 6, 0), (48, 5, 5, 0)])
 def test_decode_very_many_units(cuda_device, d, new, group, window, quant):
