@@ -292,6 +292,34 @@ def test_read(cuda_device, d, hk, page, quant):
     assert (k_out[r0 + page:r0 + 2 * page] == 5).all() and not (k_out[r0:r0 + page] == 5).all()
 
 
+@pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("d,hk", [(64, 5), (128, 3), (80, 11)])
+def test_read_many_rows(cuda_device, d, hk, quant):
+    """More rows than the groups of a full device; documents of odd lengths over shared random pages."""
+    gen = torch.Generator().manual_seed(d)
+    page, pages, lens = 16, 50, [3001, 0, 1999, 1, 4095]
+    if quant:
+        kc, vc = (torch.randint(0, 127, (pages, hk, page, d), generator=gen, dtype=torch.uint8).view(torch.float8_e4m3fn) for _ in range(2))
+        ks, vs = (torch.rand(pages, hk, page, generator=gen) for _ in range(2))
+    else:
+        kc, vc = (torch.randn(pages, hk, page, d, generator=gen).to(BF) for _ in range(2))
+        ks = vs = None
+    tab = torch.randint(0, pages, (len(lens), 4096 // page), generator=gen, dtype=torch.int32)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    total = int(cu[-1]) + 2
+    k_out, v_out = (torch.full((total, hk, d), 9.0, dtype=BF, device="cuda") for _ in range(2))
+    ksd, vsd = dev(ks, vs)
+    kda.kv_read(kc.cuda(), vc.cuda(), tab.cuda(), cu.cuda(), k_out, v_out, k_scale=ksd, v_scale=vsd)
+    for out, cache, scale in ((k_out, kc, ks), (v_out, vc, vs)):
+        got = out.cpu()
+        assert (got[-2:] == 9).all()
+        for b, n in enumerate(lens):
+            j = torch.arange(n)
+            p, r = tab[b].long()[j // page], j % page
+            want = cache[p, :, r] if scale is None else (cache[p, :, r].float() * scale[p, :, r][..., None]).to(BF)
+            assert torch.equal(bits(got[int(cu[b]):int(cu[b + 1])]), bits(want))
+
+
 # ------------------------------------------------------------------------------------ decode attention
 def run_decode(lens, new, hk, group, d, page, quant, softcap=0.0, window=0, seed=11, extra=2, scale=None, max_pages=None,
                k_std=1.0, v_std=1.0, mutate=None, repeat=False):
