@@ -1022,9 +1022,10 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
 // in a row, against 33.4.)
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kFewPartials = 8;
+constexpr int kJoinCtas = 3;  // per SM (8 sequences to 131072: 174 us, with two and as many registers 177, with four, which spills, 176)
 
 template <bool kFp8, int kDP, int kNQ, Mode kMode>
-__global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid_constant__ DecodeParams p, int grid) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtas) attn_join_kernel(const __grid_constant__ DecodeParams p, int grid) {
   using G = Geo<kFp8, kDP, kNQ, kMode>;
   constexpr int kDM = kDP / 16, kMost = G::kMaxCtas * G::kShares, kPer = (kMost + kJoinThreads - 1) / kJoinThreads;
   const AttnDecodeArgs& a = p.a;
@@ -1117,19 +1118,40 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
   for (int k = 0; k < kPer; ++k)
     if (kPer * tid + k < shares) s_end[kPer * tid + k] += before + incl - jobs;
   __syncthreads();
-  sm100::griddep_wait();
-
-  for (int job = blockIdx.x; job < total; job += gridDim.x) {
+  // A job: its unit's partials, row tile and channel tile, and where the results go.
+  int4 mt = make_int4(0, 0, 0, 0);
+  bool many = false;
+  int nq = 0, jj = 0;
+  int64_t out_g = 0, out_c[2] = {0, 0};  // the token's row of tile rows g and 2 c + {0, 1}; -1 beyond the unit's
+  auto find = [&](int job) {
     int lo = 0, hi = shares - 1;  // the first share whose end is beyond the job
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (s_end[mid] > job) hi = mid;
       else lo = mid + 1;
     }
-    const int4 mt = s_meta[lo];
+    mt = s_meta[lo];
     const int local = job - (lo > 0 ? s_end[lo - 1] : 0);
-    const bool many = mt.y > kFewPartials;
-    const int nq = many ? local / kDM : local, jj = many ? local % kDM : warp;
+    many = mt.y > kFewPartials;
+    nq = many ? local / kDM : local;
+    jj = many ? local % kDM : warp;
+    const int bh = mt.z / p.row_blocks, row_base = (mt.z - bh * p.row_blocks) * 8 * kNQ + 8 * nq;
+    const int b = bh / a.hkv, h = bh - b * a.hkv;
+    auto row_at = [&](int row) {
+      const int t = row / p.group;
+      return row < p.rows ? ((int64_t)b * a.new_tokens + t) * a.hq + h * p.group + row - t * p.group : -1;
+    };
+    out_g = row_at(row_base + g);
+    out_c[0] = row_at(row_base + 2 * c);
+    out_c[1] = row_at(row_base + 2 * c + 1);
+  };
+  // (the first one is found before the wait)
+  int job = blockIdx.x;
+  if (job < total) find(job);
+  sm100::griddep_wait();
+
+  for (; job < total; job += gridDim.x) {
+    if (job != blockIdx.x) find(job);
     const int share0 = mt.x >> 1;
     auto slot = [&](int i) { return (int64_t)(i == 0 ? mt.x : 2 * (share0 + i)) * kNQ + nq; };
     // partials first, first + step, ..: their results relative to the largest reference met so far
@@ -1176,20 +1198,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
       for (int w = 1; w < kJoinWarps; ++w) add(s_ml[w][lane], s_o[w][lane]);
     }
     if (jj < kDM) {
-      const int bh = mt.z / p.row_blocks, row_base = (mt.z - bh * p.row_blocks) * 8 * kNQ + 8 * nq;
-      const int b = bh / a.hkv, h = bh - b * a.hkv;
-      auto row_at = [&](int row) {
-        const int t = row / p.group;
-        return ((int64_t)b * a.new_tokens + t) * a.hq + h * p.group + row - t * p.group;
-      };
       float inv[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         inv[x] = l[x] == 0.f ? 0.f : 1.f / l[x];
-        const int r = row_base + 2 * c + x;
-        if (jj == 0 && g == 0 && r < p.rows && a.lse) a.lse[row_at(r)] = lse_of(m[x], l[x], kFp8 ? kWeightShift : 0.f);
+        if (jj == 0 && g == 0 && out_c[x] >= 0 && a.lse) a.lse[out_c[x]] = lse_of(m[x], l[x], kFp8 ? kWeightShift : 0.f);
       }
-      write_tile<kFp8, kDP>(o, jj, inv, row_base + g < p.rows ? a.out + row_at(row_base + g) * a.d : nullptr, a.d);
+      write_tile<kFp8, kDP>(o, jj, inv, out_g >= 0 ? a.out + out_g * a.d : nullptr, a.d);
     }
   }
 }
@@ -1239,7 +1254,7 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<kFp8, kDP, kNQ, kMode>, p);
   if (e != cudaSuccess || kMode == kWhole || most_blocks == 1) return e;  // (no unit is in two shares: nothing to join)
-  cfg.gridDim = dim3((unsigned)(2 * sms));
+  cfg.gridDim = dim3((unsigned)(kJoinCtas * sms));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<kFp8, kDP, kNQ, kMode>, p, (int)grid);
