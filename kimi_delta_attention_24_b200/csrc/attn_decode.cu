@@ -1022,7 +1022,7 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
 // in a row, against 33.4.)
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kFewPartials = 8;
-constexpr int kJoinCtas = 3;  // per SM (8 sequences to 131072: 174 us, with two and as many registers 177, with four, which spills, 176)
+constexpr int kJoinCtas = 3;  // per SM (8 sequences to 131072: 174 us, with two and more registers 177, with four, which spills, 176)
 
 template <bool kFp8, int kDP, int kNQ, Mode kMode>
 __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) attn_join_kernel(const __grid_constant__ DecodeParams p, int grid) {
@@ -1253,11 +1253,14 @@ cudaError_t launch_typed(const AttnDecodeArgs& a, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<kFp8, kDP, kNQ, kMode>, p);
-  if (e != cudaSuccess || kMode == kWhole || most_blocks == 1) return e;  // (no unit is in two shares: nothing to join)
-  cfg.gridDim = dim3((unsigned)(kJoinCtas * sms));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kFp8, kDP, kNQ, kMode>, p, (int)grid);
+  if constexpr (kMode != kWhole) {
+    if (e != cudaSuccess || most_blocks == 1) return e;  // (no unit is in two shares: nothing to join)
+    cfg.gridDim = dim3((unsigned)(kJoinCtas * sms));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<kFp8, kDP, kNQ, kMode>, p, (int)grid);
+  }
+  return e;
 }
 
 // Units per warp from which warps take shares of their own: their results of a unit need no joining
