@@ -520,8 +520,8 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* partial
 }
 
 // The rows of the packed outputs from the cache: a group of lanes takes kReadRows of the 2 heads rows (K,
-// then V) of one token.  Bound by HBM: the cache rows read once, the bf16 rows written once.
-template <int kLanes, bool kQuant, int kReadRows>
+// then V) of one token, or, with one or two heads, those of kPer consecutive tokens.  Bound by HBM: the cache rows read once, the bf16 rows written once.
+template <int kLanes, bool kQuant, int kReadRows, int kPer>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvReadArgs a) {
   constexpr int kGroups = kThreads / kLanes;
   const int sub = threadIdx.x & (kLanes - 1);
@@ -535,33 +535,45 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
     return;
   }
   const int64_t total = a.cu_seqlens[a.num_seqs];
-  const int parts = (2 * a.heads + kReadRows - 1) / kReadRows;
-  const uint32_t items = (uint32_t)(total * parts);  // (below 2^31: checked by the host)
+  constexpr int kTokenRows = kReadRows / kPer;  // (where kPer > 1 exactly the 2 heads rows of a token: so the host picks kPer)
+  const int parts = (2 * a.heads + kTokenRows - 1) / kTokenRows;
+  const uint32_t items = (uint32_t)((total + kPer - 1) / kPer * parts);  // (below 2^31: checked by the host)
+  if (8 * sub >= a.d) return;
   for (uint32_t item = blockIdx.x * kGroups + threadIdx.x / kLanes; item < items; item += gridDim.x * kGroups) {
-    const int64_t row = item / (uint32_t)parts;
-    const int r0 = (int)(item % (uint32_t)parts) * kReadRows;
+    const int64_t row0 = (int64_t)(item / (uint32_t)parts) * kPer;
+    const int r0 = (int)(item % (uint32_t)parts) * kTokenRows;
     int lo = 0, hi = a.num_seqs - 1;  // the last sequence that begins at or before the row and is not empty
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(a.cu_seqlens + mid) <= row) lo = mid;
+      if (__ldg(a.cu_seqlens + mid) <= row0) lo = mid;
       else hi = mid - 1;
     }
-    const int t = (int)(row - __ldg(a.cu_seqlens + lo));
-    const int page = __ldg(a.page_table + (int64_t)lo * a.max_pages + (t >> a.page_shift));
-    if ((uint32_t)page >= (uint32_t)a.num_pages) {
-      if (a.status) atomicOr(a.status, kStatusBadIndex);
-      continue;
+    int pages[kPer], at[kPer];  // page -1: the token is left out
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      pages[u] = -1;
+      at[u] = 0;
+      if (row0 + u >= total) continue;
+      if (u > 0)
+        while (__ldg(a.cu_seqlens + lo + 1) <= row0 + u) ++lo;
+      const int t = (int)(row0 + u - __ldg(a.cu_seqlens + lo));
+      pages[u] = __ldg(a.page_table + (int64_t)lo * a.max_pages + (t >> a.page_shift));
+      at[u] = t & ((1 << a.page_shift) - 1);
+      if ((uint32_t)pages[u] >= (uint32_t)a.num_pages) {
+        if (a.status) atomicOr(a.status, kStatusBadIndex);
+        pages[u] = -1;
+      }
     }
-    const int at = t & ((1 << a.page_shift) - 1);
-    if (8 * sub >= a.d) continue;
+    if (kPer == 1 && pages[0] < 0) continue;
     uint4 v[kReadRows];
     float sc[kReadRows];
 #pragma unroll
     for (int i = 0; i < kReadRows; ++i) {
-      const int r = r0 + i;
-      if (r >= 2 * a.heads) break;
+      const int r = r0 + i % kTokenRows, page = pages[i / kTokenRows];
+      if (kPer == 1 && r >= 2 * a.heads) break;
+      if (kPer > 1 && page < 0) continue;
       const bool is_v = r >= a.heads;
-      const int64_t line = ((int64_t)(is_v ? r - a.heads : r) << a.page_shift) + at;
+      const int64_t line = ((int64_t)(is_v ? r - a.heads : r) << a.page_shift) + at[i / kTokenRows];
       const int64_t off = (int64_t)page * (is_v ? a.v_page_stride : a.k_page_stride) + line * a.d + 8 * sub;
       const void* cache = is_v ? a.v_cache : a.k_cache;
       if (kQuant) {
@@ -574,8 +586,9 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
     }
 #pragma unroll
     for (int i = 0; i < kReadRows; ++i) {
-      const int r = r0 + i;
-      if (r >= 2 * a.heads) break;
+      const int r = r0 + i % kTokenRows;
+      if (kPer == 1 && r >= 2 * a.heads) break;
+      if (kPer > 1 && pages[i / kTokenRows] < 0) continue;
       const bool is_v = r >= a.heads;
       if (kQuant) {
         const uint32_t w[2] = {v[i].x, v[i].y};
@@ -588,7 +601,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
         }
         v[i] = to_bf16(x);
       }
-      __nv_bfloat16* out = (is_v ? a.v_out : a.k_out) + (row * a.heads + (is_v ? r - a.heads : r)) * a.d + 8 * sub;
+      __nv_bfloat16* out = (is_v ? a.v_out : a.k_out) + ((row0 + i / kTokenRows) * a.heads + (is_v ? r - a.heads : r)) * a.d + 8 * sub;
       __stcs(reinterpret_cast<uint4*>(out), v[i]);
     }
   }
@@ -686,11 +699,19 @@ cudaError_t launch_kv_read(const KvReadArgs& a, cudaStream_t stream) {
   // tokens 3.3 us with eight and 3.0 with four, 8000 tokens 10.5 and 11.1; e4m3, 8000: 10.5 and 12.1).
   auto blocks = [&](int rows) { return (a.total * ((2 * a.heads + rows - 1) / rows) * lanes + kThreads - 1) / kThreads; };
   const bool few = blocks(8) < 2 * (int64_t)sms;
-  const int64_t grid = std::min<int64_t>(blocks(few ? 4 : 8), 16 * sms);
+  // One or two heads: the eight rows are of four or two tokens, where that leaves the device full (128000
+  // tokens of one head of 64: bf16 16.7 us with one token and 12.2 with four, e4m3 17.6 and 13.5).
+  const int tokens = a.heads > 2 ? 1 : 4 / a.heads;
+  const int per = blocks(8) / tokens < 2 * (int64_t)sms ? 1 : tokens;
+  const int64_t grid = std::min<int64_t>((blocks(few ? 4 : 8) + per - 1) / per, 16 * sms);
   auto pick = [&](auto quant) {
     constexpr bool kQuant = decltype(quant)::value;
-    return lanes == 8 ? (few ? kv_read_kernel<8, kQuant, 4> : kv_read_kernel<8, kQuant, 8>)
-                      : (few ? kv_read_kernel<16, kQuant, 4> : kv_read_kernel<16, kQuant, 8>);
+    auto form = [&](auto l) {
+      constexpr int kLanes = decltype(l)::value;
+      return few ? kv_read_kernel<kLanes, kQuant, 4, 1> : per == 4 ? kv_read_kernel<kLanes, kQuant, 8, 4>
+           : per == 2 ? kv_read_kernel<kLanes, kQuant, 8, 2> : kv_read_kernel<kLanes, kQuant, 8, 1>;
+    };
+    return lanes == 8 ? form(std::integral_constant<int, 8>()) : form(std::integral_constant<int, 16>());
   };
   (a.k_scale ? pick(std::true_type()) : pick(std::false_type()))<<<(unsigned)grid, kThreads, 0, stream>>>(a);
   return cudaGetLastError();

@@ -293,18 +293,19 @@ def test_read(cuda_device, d, hk, page, quant):
 
 
 @pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
-@pytest.mark.parametrize("d,hk", [(64, 5), (128, 3), (80, 11)])
-def test_read_many_rows(cuda_device, d, hk, quant):
+@pytest.mark.parametrize("d,hk,longest", [(64, 5, 9001), (128, 3, 9001), (80, 11, 3001), (128, 1, 30001), (128, 2, 30001), (64, 1, 30001),
+                                          (48, 2, 30001), (64, 1, 9001), (64, 2, 9001), (128, 1, 9001)])
+def test_read_many_rows(cuda_device, d, hk, longest, quant):
     """More rows than the groups of a full device; documents of odd lengths over shared random pages."""
     gen = torch.Generator().manual_seed(d)
-    page, pages, lens = 16, 50, [3001, 0, 1999, 1, 4095]
+    page, pages, lens = 16, 50, [longest, 0, 1999, 1, 0, 2, 16383]
     if quant:
         kc, vc = (torch.randint(0, 127, (pages, hk, page, d), generator=gen, dtype=torch.uint8).view(torch.float8_e4m3fn) for _ in range(2))
         ks, vs = (torch.rand(pages, hk, page, generator=gen) for _ in range(2))
     else:
         kc, vc = (torch.randn(pages, hk, page, d, generator=gen).to(BF) for _ in range(2))
         ks = vs = None
-    tab = torch.randint(0, pages, (len(lens), 4096 // page), generator=gen, dtype=torch.int32)
+    tab = torch.randint(0, pages, (len(lens), 1876), generator=gen, dtype=torch.int32)
     cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
     total = int(cu[-1]) + 2
     k_out, v_out = (torch.full((total, hk, d), 9.0, dtype=BF, device="cuda") for _ in range(2))
