@@ -474,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
           const Row8 x = to_float(cx[i]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (live) dw[j] = fma2(mul2(g[i].v[j], r2), x.v[j], dw[j]);  // (a skipped token adds nothing)
+            // (a skipped token adds nothing, nor does a place behind the last head: r is infinite there where eps is 0)
+            if (live && head0 + i < in.heads) dw[j] = fma2(mul2(g[i].v[j], r2), x.v[j], dw[j]);
             out.v[j] = fma2(x.v[j], k2, mul2(mul2(g[i].v[j], w[j]), r2));
           }
         }

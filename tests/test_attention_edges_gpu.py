@@ -1,0 +1,41 @@
+"""Corners of the softmax-attention operators that their documentation allows, against the formulas in 64 bits
+(attention_ref.py, which derives the tolerances)."""
+import pytest
+import torch
+
+import attention_ref as ref
+import kimi_delta_attention_24_b200 as kda
+from test_attention_gpu import BF, dev, within
+
+pytestmark = pytest.mark.gpu
+
+
+def bwd_inputs(tokens, hq, hk, d, rot, seed):
+    g = torch.Generator().manual_seed(seed)
+    qkv = torch.randn(tokens, hq + 2 * hk, d, generator=g).to(BF)
+    wq, wk = (1 + 0.3 * torch.randn(d, generator=g) for _ in range(2))
+    tab = ref.table(rot, 500) if rot else None
+    pos = torch.randint(1, 500, (tokens,), generator=g, dtype=torch.int32) if rot else None
+    gq, gk = (torch.randn(tokens, h, d, generator=g).to(BF) for h in (hq, hk))
+    return qkv[:, :hq], qkv[:, hq:hq + hk], wq, wk, tab, pos, gq, gk
+
+
+# ------------------------------------------------------------------------------------ the gradient
+# The weights' gradients: at the sizes here a lane adds up to 32 rows, a block up to 32 lanes, and the last
+# launch 35 blocks' sums in each of 8 slices; with the 14 roundings of a term below 128 units of 2^-24 (the
+# reference's tolerance counts 96).
+DW_MORE = 128 / 96
+
+
+@pytest.mark.parametrize("tokens,hq,hk,d,rot", [
+    (1, 1, 1, 64, 64), (5, 5, 1, 128, 64), (33, 9, 2, 80, 80), (300, 13, 7, 128, 0),
+    # enough tokens for several turns of two heads each, and heads that do not fill them
+    (3301, 20, 1, 128, 128), (3301, 18, 3, 128, 64), (6701, 24, 1, 64, 32)])
+def test_bwd_without_epsilon(cuda_device, tokens, hq, hk, d, rot):
+    """eps = 0: 1 / sqrt(mean x^2) of the places behind the last head, which hold no row, is infinite."""
+    q, k, wq, wk, tab, pos, gq, gk = bwd_inputs(tokens, hq, hk, d, rot, 51)
+    r = kda.qk_norm_rope_bwd(*dev(gq, gk, q, k, wq, wk), 0.0, *dev(tab, pos))
+    for n, x, w, dy in (("q", q, wq, gq), ("k", k, wk, gk)):
+        dx, dw, dx_tol, dw_tol = ref.norm_rope_bwd(x, w, 0.0, tab, pos, False, dy)
+        within(r["d" + n], dx, dx_tol, "d" + n)
+        within(r[f"d{n}_weight"], dw, dw_tol * DW_MORE, f"d{n}_weight")
