@@ -324,7 +324,8 @@ kda_status_t kda_bwd(const void* q, const void* k, const void* v, const void* g,
  * Device-side checks.  Positions, slots, page numbers and lengths live on the device.  What is out of
  * range there is never read or written through; it is recorded as KDA_ERR_INVALID_ARGUMENT in the
  * workspace's status word (kda_read_device_status), and
- *   - a token whose position or slot is out of range is skipped: its output rows stay as they were;
+ *   - a token whose position or slot is out of range is skipped: its output rows stay as they were (in
+ *     the gradient, which it has no part in, its rows become zero);
  *   - a length below 0 counts as 0, one beyond the table (max_pages * page_size) as that;
  *   - kda_kv_read leaves the rows of a page number out of range, and kda_attn_decode reads page 0 in
  *     its place (that sequence's results are then meaningless).

@@ -78,7 +78,7 @@ def qk_norm_rope_bwd(d_q_out, d_k_out, q, k, q_weight=None, k_weight=None, eps=1
                      interleaved=False, workspace=None, stream=None):
     """Gradients of sum(d_q_out * q_out) + sum(d_k_out * k_out) of ``qk_norm_rope``: a dict of dq, dk
     (bf16, contiguous) and dq_weight, dk_weight (fp32 [D]; None where the weight is None).  ``q`` or
-    ``k`` may be None, with its gradient."""
+    ``k`` may be None, with its gradient.  A token whose position is out of range has gradients of zero."""
     return (_binding or _load()).qk_norm_rope_bwd(d_q_out, d_k_out, q, k, q_weight, k_weight, eps, cos_sin, positions,
                                                     interleaved, workspace, stream)
 

@@ -479,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
             out.v[j] = fma2(x.v[j], k2, mul2(mul2(g[i].v[j], w[j]), r2));
           }
         }
-        if (live && lane_on0 && head0 + i < in.heads)
-          *reinterpret_cast<uint4*>(dx + (token * in.heads + head0 + i) * a.d + 8 * sub) = to_bf16(out);
+        if (here && lane_on0 && head0 + i < in.heads)  // (a skipped token: zeros)
+          *reinterpret_cast<uint4*>(dx + (token * in.heads + head0 + i) * a.d + 8 * sub) = live ? to_bf16(out) : make_uint4(0, 0, 0, 0);
       }
     }
     pos = next_pos;

@@ -1,5 +1,7 @@
 """Corners of the softmax-attention operators that their documentation allows, against the formulas in 64 bits
 (attention_ref.py, which derives the tolerances)."""
+import math
+
 import pytest
 import torch
 
@@ -39,3 +41,28 @@ def test_bwd_without_epsilon(cuda_device, tokens, hq, hk, d, rot):
         dx, dw, dx_tol, dw_tol = ref.norm_rope_bwd(x, w, 0.0, tab, pos, False, dy)
         within(r["d" + n], dx, dx_tol, "d" + n)
         within(r[f"d{n}_weight"], dw, dw_tol * DW_MORE, f"d{n}_weight")
+
+
+@pytest.mark.parametrize("d,rot,hq,hk", [(64, 64, 3, 1), (128, 64, 4, 2)])
+def test_bwd_of_skipped_tokens(cuda_device, d, rot, hq, hk):
+    """A token whose position is out of range has no output, so its gradients are zero, whatever its rows hold;
+    it adds nothing to the weights' gradients, and the status word tells of it."""
+    tokens = 45
+    q, k, wq, wk, tab, pos, gq, gk = bwd_inputs(tokens, hq, hk, d, rot, 52)
+    off = torch.zeros(tokens, dtype=torch.bool)
+    off[[0, 7, 8, 44]] = True
+    pos[0], pos[7], pos[8], pos[44] = 500, -1, 1 << 30, -(1 << 31)
+    q[7, 1, 3], k[8, 0, 5], gq[44, 0, 0], gk[0, 0, 1] = math.nan, math.inf, math.nan, -math.inf
+    ws = torch.zeros(kda.load().kda_qk_norm_rope_bwd_workspace_size(), dtype=torch.uint8, device="cuda")
+    args = dev(gq, gk, q, k, wq, wk), dev(tab, pos)
+    # (memory that earlier tensors left behind would show in rows that are not written)
+    left = [torch.full((tokens, h, d), 7.0, dtype=BF, device="cuda") for h in (hq, hk)]
+    del left
+    r = kda.qk_norm_rope_bwd(*args[0], 1e-6, *args[1], workspace=ws)
+    assert kda.read_device_status(ws) == 1 and kda.read_device_status(ws) == 0
+    for n, x, w, dy in (("q", q, wq, gq), ("k", k, wk, gk)):
+        dx, dw, dx_tol, dw_tol = ref.norm_rope_bwd(x[~off], w, 1e-6, tab, pos[~off], False, dy[~off])
+        got = r["d" + n].cpu()
+        within(got[~off], dx, dx_tol, "d" + n)
+        assert (got[off] == 0).all()
+        within(r[f"d{n}_weight"], dw, dw_tol, f"d{n}_weight")
