@@ -316,7 +316,7 @@ kda_status_t kda_bwd(const void* q, const void* k, const void* v, const void* g,
  * v_page_stride elements apart (16 bytes' multiple, at least num_kv_heads * page_size * D, below
  * 2^38), page_size a power of two from 8 to 1024, num_pages * page_size < 2^31.  Either bf16 (k_scale
  * and v_scale NULL), or e4m3 codes with fp32 scales k_scale, v_scale [num_pages][num_kv_heads]
- * [page_size] (contiguous), one per row: a row's values are code * scale.
+ * [page_size] (contiguous), one per row, finite and not negative, or NaN: a row's values are code * scale.
  *   Slot s is row s % page_size of page s / page_size.  A sequence's tokens 0, 1, .. lie in the pages
  * of its page_table row [max_pages] in order; entries beyond its last page are not read.
  *   16-byte aligned: every bf16 tensor, the caches, weights and the rotation table; the others 4-byte.
@@ -411,8 +411,16 @@ size_t kda_attn_decode_workspace_size(int32_t new_tokens, int32_t num_q_heads, i
  *               Sequences may share pages.  With a window, entries of pages before it are not read.
  *   workspace   kda_attn_decode_workspace_size bytes, 256-byte aligned; calls that share one must be
  *               ordered (the same stream, or events).
- * One pass over the cache in two launches (one, where few sequences can have few keys each); fp32
- * scores, softmax statistics and sums.  The order of all sums is fixed by the sizes and lengths. */
+ * Two launches (one, where few sequences can have few keys each); the cache is read once for every 16
+ * rows (new_tokens * num_q_heads / num_kv_heads) of a kv head.  fp32 scores, softmax statistics and
+ * sums; the order of all sums is fixed by the sizes and lengths.  What is rounded to fewer bits on the way:
+ *   - bf16 cache: a key's weight, to a pair of bf16 (2^-17 of it);
+ *   - e4m3 cache: a key's weight times its value scale, to fp16 relative to the row's largest such product (2^-11
+ *     of it, at worst 2^-38 of the largest); a row of q, to fp16 relative to its largest channel (exact for
+ *     channels down to 2^-17 of that one).
+ * e4m3 cache: value scales below 2^-80 count as that, and the scales of the rows that a query sees are to lie
+ * within a factor of 2^90 of one another (written by kda_kv_append they do, if no value passes 2^34 in
+ * magnitude); beyond it keys of the smallest scales may drop out of the sums. */
 kda_status_t kda_attn_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                              const float* v_scale, const int32_t* page_table, const int32_t* seq_lens, float scale,
                              float softcap, int32_t window, void* out, float* lse, int32_t batch, int32_t new_tokens,

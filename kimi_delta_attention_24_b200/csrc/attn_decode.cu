@@ -24,12 +24,14 @@
 //     at T = 1) wastes half as much of each instruction, and half the registers, as with 16 rows.
 //   - What remains to be hidden is latency: two or three warps per scheduler take 2600 to 3500 cycles a tile
 //     whether its bytes have arrived or not.  So dependent products are kept apart, and the softmax
-//     exchanges maxima between threads only when a score passes its row's reference by 2^8.
+//     exchanges maxima between threads only when a score passes its row's reference by 2^8 (e4m3 cache: 2).
 //   - bf16 cache: P enters the second product as a bf16 pair hi + lo, so its rounding (2^-17) stays
 //     below that of the bf16 output.  e4m3 cache: codes are exact in fp16; the key's scale multiplies
 //     the score, and the value's enters the exponent, w_j = 2^(z_j + log2 s_j - M) with M the row's
-//     reference of that sum (within 2^8 of its maximum), whatever the scales are; times 2^7 it is rounded
-//     to fp16 (2^-11 down to 2^-21 of 2^M).  q (bf16) is scaled by a power of two per row to fit fp16.
+//     reference of that sum (within 2 of its maximum); times 2^14 it is rounded to fp16 (2^-11 down to
+//     2^-28 of 2^M, at worst by 2^-39 of it; moving M only past 2^8, times 2^7, costs 2^7 of that and saves 1.0 us
+//     of 174.7 at 8 sequences to 131072, 0.5 of 32.5 at 48 to 8192).  The row's sum adds w_j / s_j in fp32 before that
+//     rounding.  q (bf16) is scaled by a power of two per row to fit fp16.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -46,8 +48,11 @@ enum Mode { kCommon, kSolo, kWhole };
 
 constexpr int kMaxSms = 160;               // bound used for the workspace (148 on a B200)
 constexpr int kMaxShares = kMaxSms * 2 * 4;  // (kSolo)
-constexpr float kLazy = 8.0f;         // how far (base 2) a score passes a row's reference before it moves
-constexpr float kWeightShift = 7.0f;  // fp16 weights: up to 2^(kLazy + kWeightShift) = 2^15
+// How far (base 2) a score passes a row's reference before it moves, by the type of cache: fp32 weights
+// may grow; fp16 weights, times 2^kWeightShift, go up to 2^15, and what they may grow is lost at their lower end.
+constexpr float kLazyBf16 = 8.0f, kLazyE4m3 = 1.0f;
+constexpr float kWeightShift = 14.0f;
+constexpr float kScaleLeast = 0x1p-80f;  // of a value row
 
 struct DecodeParams {
   AttnDecodeArgs a;
@@ -580,10 +585,11 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
       if (kFp8) {
         // once per key: the logarithm of its value scale and the reciprocal.  (A scale that is not a
         // number makes the rows that see its key so, by way of the logarithm; its reciprocal stays
-        // finite, for the rows that do not see it.)
+        // finite, for the rows that do not see it.  Scales below 2^-80, which no write to the cache makes, count
+        // as that: 2^15 w_j / s_j of 2^30 keys add up to less than fp32's largest.)
         const float v = sc[kTok + lane];
-        sc[kTok + lane] = lg2_approx(v < 0x1p-100f ? 0x1p-100f : v);
-        sc[2 * kTok + lane] = rcp_approx(fmaxf(v, 0x1p-100f));
+        sc[kTok + lane] = lg2_approx(v < kScaleLeast ? kScaleLeast : v);
+        sc[2 * kTok + lane] = rcp_approx(fmaxf(v, kScaleLeast));
         __syncwarp();
       }
       const int t0 = tok0 + i * G::kBlockTok;
@@ -703,7 +709,7 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
       }
       // ---- running sum and reference of the exponents; P in place of S.  The reference m of a row is
       // its maximum when it was last moved: it moves (for all rows of the warp) only when a score
-      // passes it by kLazy, so P stays below 2^kLazy and most tiles need no exchange between lanes.
+      // passes it by kLazy, so P stays below 2^kLazy (e4m3: 2^15 with its shift) and most tiles need no exchange between lanes.
       float mx[kNQ][2];
       bool passed = false;
 #pragma unroll
@@ -714,7 +720,7 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
 #pragma unroll
           for (int kt = 0; kt < kKT; ++kt) mx[nq][x] = fmaxf(mx[nq][x], fmaxf(s[kt][nq][x], s[kt][nq][x + 2]));
           mx[nq][x] *= kFp8 || capped ? 1.f : rscale[nq][x];
-          passed |= mx[nq][x] > m[nq][x] + kLazy;
+          passed |= mx[nq][x] > m[nq][x] + (kFp8 ? kLazyE4m3 : kLazyBf16);
         }
       if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll

@@ -66,3 +66,51 @@ def test_bwd_of_skipped_tokens(cuda_device, d, rot, hq, hk):
         within(got[~off], dx, dx_tol, "d" + n)
         assert (got[off] == 0).all()
         within(r[f"d{n}_weight"], dw, dw_tol, f"d{n}_weight")
+
+
+# ------------------------------------------------------------------------------------ decode attention
+def test_decode_small_weights_keep_their_bits(cuda_device):
+    """e4m3 cache: channels to which only keys of weights 2^-22 to 2^-27 of the largest add.  A weight is rounded to
+    fp16 as p s 2^14 relative to a reference within a factor of two of the largest: 2^-11 of it down to 2^-28 of the
+    reference, so here as for the large ones."""
+    gen = torch.Generator().manual_seed(71)
+    n, d, page, group = 3, 64, 16, 4
+    for drop in (22, 23, 24, 25, 26, 26, 27, 27):
+        kc, ks = ref.make_cache(gen, 2, 1, page, d, True)
+        vc, vs = ref.make_cache(gen, 2, 1, page, d, True)
+        tab = ref.fill_sequences(gen, [n], kc, vc, ks, vs)
+        q = torch.zeros(1, 1, group, d, dtype=BF)
+        q[..., 0] = 1.0
+        j = torch.arange(n)
+        p, r = tab[0].long()[j // page], j % page
+        # scores: 0 for the first key, about -drop ln 2 for the others; values: the first key's in channel 0 alone
+        k = torch.zeros(n, d)
+        k[1:, 0] = -drop * math.log(2.0) * (1 + 0.02 * torch.rand(n - 1, generator=gen))
+        v = 1 + torch.rand(n, d, generator=gen)
+        v[0, 1:], v[1:, 0] = 0, 0
+        for cache, scale, x in ((kc, ks, k), (vc, vs, v)):
+            c, s = ref.quantise(x)
+            cache.view(torch.uint8)[p, 0, r] = c.view(torch.uint8)
+            scale[p, 0, r] = s
+        args = [t.cuda() for t in (q, kc, vc, tab, torch.tensor([n], dtype=torch.int32))]
+        out = kda.attn_decode(*args, 1.0, k_scale=ks.cuda(), v_scale=vs.cuda())
+        o, _, _, _ = ref.attention(q, kc, vc, tab, [n], 1.0, ks, vs)
+        # the output's rounding, a weight's (2^-11), and below 2^-14 for scores, exponentials and sums (all terms
+        # of a channel have one sign); 2^-39 of the largest p s (s 448 <= 2) for each key that is subnormal
+        tol = (ref.BF16 + (1 + ref.BF16) * (2.0 ** -11 + 2.0 ** -14)) * o.abs() + n * 2.0 ** -38
+        within(out, o, tol, f"weights of 2^-{drop}")
+
+
+@pytest.mark.parametrize("n", [1, 300, 20000])
+def test_decode_zeroed_cache(cuda_device, n):
+    """A cache of zeros, its scales zero too: every key alike, out 0 and lse log n."""
+    kc = torch.zeros(1, 2, 64, 64, device="cuda").to(torch.float8_e4m3fn)
+    ks = torch.zeros(1, 2, 64, device="cuda")
+    table = torch.zeros(1, 320, dtype=torch.int32, device="cuda")
+    lse = torch.zeros(1, 4, device="cuda")
+    q = torch.ones(1, 4, 64, dtype=BF, device="cuda")
+    out = kda.attn_decode(q, kc, kc, table, torch.tensor([n], dtype=torch.int32, device="cuda"), 0.125, k_scale=ks, v_scale=ks, lse=lse)
+    assert (out == 0).all()
+    # sums of n equal terms (their rounding is below n 2^-24, and a term's below 2^-20), a scale's logarithm of -80
+    want = torch.full((1, 4), math.log(n), dtype=torch.float64)
+    within(lse, want, torch.full_like(want, (n + 300) * ref.F32 + 2.0 ** -20 + 100 * 4 * ref.F32), "lse")
