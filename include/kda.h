@@ -416,8 +416,8 @@ size_t kda_attn_decode_workspace_size(int32_t new_tokens, int32_t num_q_heads, i
  * sums; the order of all sums is fixed by the sizes and lengths.  What is rounded to fewer bits on the way:
  *   - bf16 cache: a key's weight, to a pair of bf16 (2^-17 of it);
  *   - e4m3 cache: a key's weight times its value scale, to fp16 relative to the row's largest such product (2^-11
- *     of it, at worst 2^-38 of the largest); a row of q, to fp16 relative to its largest channel (exact for
- *     channels down to 2^-17 of that one).
+ *     of it, at worst 2^-38 of the largest); a row of q, to fp16 relative to its largest channel, or to 2^-100
+ *     (exact for channels down to 2^-17 of that).
  * e4m3 cache: value scales below 2^-80 count as that, and the scales of the rows that a query sees are to lie
  * within a factor of 2^90 of one another (written by kda_kv_append they do, if no value passes 2^34 in
  * magnitude); beyond it keys of the smallest scales may drop out of the sums. */

@@ -541,9 +541,10 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
           }
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          // the power of two below the row's largest magnitude (exact factors)
+          // the power of two below the row's largest magnitude, whose inverse is a normal number too (exact
+          // factors; a row with an infinity or NaN is that whatever the factor)
           int e = (int)((__float_as_uint(big) >> 23) & 255) - 127;
-          e = big == 0.f || e > 126 ? 0 : (e < -100 ? -100 : e);
+          e = big == 0.f || e > 127 ? 0 : min(max(e, -100), 126);
           const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
           for (int x = 0; x < 2; ++x) rscale[nq][x] = base_scale * __shfl_sync(0xffffffffu, up, 4 * (2 * c + x));

@@ -7,7 +7,7 @@ import torch
 
 import attention_ref as ref
 import kimi_delta_attention_24_b200 as kda
-from test_attention_gpu import BF, dev, within
+from test_attention_gpu import BF, dev, run_decode, within
 
 pytestmark = pytest.mark.gpu
 
@@ -69,6 +69,22 @@ def test_bwd_of_skipped_tokens(cuda_device, d, rot, hq, hk):
 
 
 # ------------------------------------------------------------------------------------ decode attention
+def test_decode_largest_queries(cuda_device):
+    """Queries up to bf16's largest power of two, against keys as small."""
+    def mutate(q, kc, vc, ks, vs, tab):
+        q *= 2.0 ** 124
+        q[..., 3] = torch.where(q[..., 3] > 0, 2.0 ** 127, -2.0 ** 127).to(BF)
+        q[0, 0, 1, 4] = 1.5 * 2.0 ** 127
+        if ks is not None:
+            ks *= 2.0 ** -60
+        else:
+            kc *= 2.0 ** -60
+    for quant in (False, True):
+        out, lse, o, l, ot, lt = run_decode([200, 17], 1, 1, 4, 128, 16, quant, mutate=mutate, scale=2.0 ** -66)
+        within(out, o, ot, "out")
+        within(lse, l, lt, "lse")
+
+
 def test_decode_small_weights_keep_their_bits(cuda_device):
     """e4m3 cache: channels to which only keys of weights 2^-22 to 2^-27 of the largest add.  A weight is rounded to
     fp16 as p s 2^14 relative to a reference within a factor of two of the largest: 2^-11 of it down to 2^-28 of the
