@@ -405,6 +405,8 @@ size_t kda_attn_decode_workspace_size(int32_t new_tokens, int32_t num_q_heads, i
  * that are NaN themselves in rows that some other query of the sequence sees (kda_kv_append writes none).
  * An infinity or NaN in a row that it sees gives NaN or an infinity where the formula has either (with an
  * e4m3 cache in lse too).
+ *   scale       zero, or such that scale * log2(e), with a cap scale / softcap, is a normal fp32 number;
+ *   softcap     zero for none, or such that softcap * log2(e) is finite (KDA_ERR_INVALID_ARGUMENT otherwise)
  *   q, out      bf16 [batch][new_tokens][num_q_heads][D] (out not in q's place);  lse fp32
  *               [batch][new_tokens][num_q_heads] or NULL
  *   page_table  int32 [batch][max_pages] (max_pages * page_size <= 2^30), seq_lens int32 [batch].

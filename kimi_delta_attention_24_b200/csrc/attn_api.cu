@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "attn_common.cuh"
+#include "kda_device.cuh"
 
 namespace {
 
@@ -47,6 +48,14 @@ kda_status_t check_cache(const void* k_cache, const void* v_cache, const float* 
   for (int64_t s : {k_page_stride, v_page_stride})
     if (s < page || s % align != 0 || s >= (int64_t)1 << 38) return KDA_ERR_INVALID_ARGUMENT;
   return KDA_OK;
+}
+
+// The factors that scores are multiplied with, in the kernel's units (base 2, with a cap the cap's): normal
+// fp32 numbers, or zero for a scale of zero.  (A product that overflows or loses bits would change the scores.)
+bool factors_ok(float scale, float softcap) {
+  if (!isfinite(scale) || !(softcap >= 0.f) || !isfinite(softcap * kda::kLog2e)) return false;
+  const float factor = softcap > 0.f ? scale / softcap : scale * kda::kLog2e;
+  return scale == 0.f || isnormal(factor);
 }
 
 int log2_of(int32_t n) {
@@ -241,8 +250,7 @@ kda_status_t kda_attn_decode(const void* q, const void* k_cache, const void* v_c
   if (batch < 0 || new_tokens < 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_pages < 0 ||
       (int64_t)max_pages * page_size > 1 << 30 || window < 0)
     return KDA_ERR_INVALID_ARGUMENT;
-  if (!isfinite(scale) || !(softcap >= 0.f && isfinite(softcap)) || (softcap > 0.f && !isfinite(scale / softcap)))
-    return KDA_ERR_INVALID_ARGUMENT;
+  if (!factors_ok(scale, softcap)) return KDA_ERR_INVALID_ARGUMENT;
   const int64_t rows = (int64_t)new_tokens * (num_q_heads / num_kv_heads);
   // (rows, units and the rows' indexes are int32; a unit is a sequence's kv head and 8 or 16 of its rows)
   if (rows > 1 << 20 || (int64_t)batch * num_kv_heads > INT32_MAX / (rows / 16 + 1) ||

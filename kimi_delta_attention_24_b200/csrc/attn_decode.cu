@@ -367,9 +367,8 @@ __global__ void __launch_bounds__(Geo<kFp8, kDP, kNQ, kMode>::kThreads, Geo<kFp8
 
   const int page_mask = (1 << a.page_shift) - 1;
   // scores to base 2 (to the cap's units): a positive factor, its sign goes to the queries, so that
-  // maxima can be taken before it (a factor of zero: zero queries)
-  const float base_scale =
-      a.scale == 0.f ? 1.f : fmaxf(fabsf(a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e), 1.17549435e-38f);
+  // maxima can be taken before it (a scale of zero: zero queries; else a normal number, by the host's check)
+  const float base_scale = a.scale == 0.f ? 1.f : fabsf(a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e);
   const uint32_t q_sign = a.scale < 0.f ? 0x80008000u : 0u, q_keep = a.scale == 0.f ? 0u : 0xffffffffu;
 
   // ---- the loading side: a ring of stages, kept full across the units' ends
