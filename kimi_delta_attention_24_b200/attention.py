@@ -7,8 +7,8 @@ kda_kv_read and kda_attn_decode entry points of libkda_b200.so (include/kda.h ha
     kv_read(k_cache, v_cache, page_table, ...)       cached rows read back
     attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale, ...)   attention over the cache
 
-Argument marshalling only, in lib/attn_binding.so (csrc/attn_binding.cpp: a call of a few microseconds
-on the GPU would spend several times that in Python).  Caches are [num_pages, num_kv_heads, page_size,
+Argument marshalling only, in lib/attn_binding.*.so (csrc/attn_binding.cpp: a call of a few microseconds on
+the GPU would spend several times that in Python).  Caches are [num_pages, num_kv_heads, page_size,
 D], bf16 or float8_e4m3fn with fp32 scales [num_pages, num_kv_heads, page_size]; pages may lie apart (any
 stride of the first dimension).  Every call runs on ``stream`` (the current stream when None) of the
 tensors' device; what a call allocates belongs to that stream.  Wrong tensors raise ValueError, what the
@@ -26,7 +26,6 @@ import torch
 __all__ = ["qk_norm_rope", "qk_norm_rope_bwd", "kv_append", "kv_read", "attn_decode", "attn_decode_workspace_size",
            "new_attn_decode_workspace"]
 
-_BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "attn_binding.so")
 # in the order attn_binding.init takes their addresses
 _FUNCTIONS = ("kda_qk_norm_rope", "kda_qk_norm_rope_bwd", "kda_qk_norm_rope_bwd_workspace_size", "kda_kv_append", "kda_kv_read",
               "kda_attn_decode", "kda_attn_decode_workspace_size")
@@ -50,13 +49,15 @@ def _declare(lib):
 
 
 def _load():
-    """Loads attn_binding.so and gives it the library's functions.  Raises if it has not been built."""
+    """Loads the binding and gives it the library's functions.  Raises if it has not been built for this torch
+    and this Python."""
     global _binding
-    from . import KDAError, load
+    from . import KDAError, build, load
     lib = load()
-    if not os.path.exists(_BINDING_PATH):
-        raise RuntimeError(f"{_BINDING_PATH} is not built; run `python -m kimi_delta_attention_24_b200.build`")
-    spec = importlib.util.spec_from_file_location("attn_binding", _BINDING_PATH)
+    path = build.binding_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built; run `python -m kimi_delta_attention_24_b200.build`")
+    spec = importlib.util.spec_from_file_location("attn_binding", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     module.init(KDAError, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _FUNCTIONS))
