@@ -300,9 +300,10 @@ kda_status_t kda_bwd(const void* q, const void* k, const void* v, const void* g,
                      int32_t head_dim_k, int32_t head_dim_v, int32_t num_seqs, kda_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------------
- * Softmax attention beside the KDA layers.  Models that use KDA interleave it with ordinary
- * (grouped-query) softmax-attention layers; these entry points run those layers' serving step next
- * to kda_decode, and the gradient of their norm + rotation for training:
+ * Softmax attention beside the KDA layers, for models whose other layers are ordinary grouped-query
+ * softmax attention (keys and values of each head as rows of up to 128 channels; a latent cache row that all
+ * heads share is not served): those layers' decoding step next to kda_decode, and the gradient of their
+ * norm + rotation for training:
  *     kda_qk_norm_rope (+ _bwd)   per-head RMS norm of queries and keys, then the position rotation
  *     kda_kv_append               the same, with keys and values written into a paged cache
  *     kda_kv_read                 cached rows read back

@@ -12,7 +12,8 @@ the GPU would spend several times that in Python).  Caches are [num_pages, num_k
 D], bf16 or float8_e4m3fn with fp32 scales [num_pages, num_kv_heads, page_size]; pages may lie apart (any
 stride of the first dimension).  Every call runs on ``stream`` (the current stream when None) of the
 tensors' device; what a call allocates belongs to that stream.  Wrong tensors raise ValueError, what the
-library refuses KDAError.
+library refuses KDAError.  No call is recorded by autograd: its results have no grad_fn, also where an input
+requires a gradient (for training, qk_norm_rope_bwd is the gradient to call).
 """
 from __future__ import annotations
 
@@ -70,7 +71,9 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, cos_sin=None, pos
     """RMS norm of every head of ``q`` and ``k`` (bf16 [..., heads, D], heads contiguous, tokens any one
     stride apart), then the rotation by the tokens' ``positions`` (int32) in ``cos_sin`` (fp32
     [max_positions, rot_dim]: cosines, then sines).  A weight (fp32 [D]) of None leaves its norm out, a
-    ``cos_sin`` of None the rotation; ``q`` or ``k`` may be None.  Returns (q_out, k_out), contiguous."""
+    ``cos_sin`` of None the rotation; ``q`` or ``k`` may be None.  Returns (q_out, k_out), contiguous; the rows
+    of a token whose position is out of range are not written (where the call allocates them, they hold
+    anything).  Not recorded by autograd."""
     return (_binding or _load()).qk_norm_rope(q, k, q_weight, k_weight, eps, cos_sin, positions, interleaved, q_out, k_out,
                                                 workspace, stream)
 
@@ -89,7 +92,7 @@ def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, q=None,
     """Norm and rotation as ``qk_norm_rope``; the keys, and ``v`` as it is, go to rows ``slots`` (int32,
     one per token, page * page_size + row; negative: the token is skipped) of the paged cache, quantised
     with a scale per row where the cache is float8_e4m3fn.  Returns q_out (None without ``q``); skipped
-    tokens' rows of a given ``q_out`` stay as they were."""
+    tokens' rows of a given ``q_out`` stay as they were (of one that the call allocates, they hold anything)."""
     return (_binding or _load()).kv_append(k, v, k_cache, v_cache, slots, k_scale, v_scale, q, q_out, q_weight, k_weight, eps,
                                              cos_sin, positions, interleaved, workspace, stream)
 

@@ -3,11 +3,12 @@
 // Row r = (new token t, query head) of a sequence and its kv head h sees the keys j of the cache with
 // j <= p (p = len - new + t, its own position) and, with a window W, j > p - W:
 //     z_j = scale q . K_j,  capped: z = cap tanh(z / cap);   o = sum_j e^{z_j} V_j / sum_j e^{z_j}
-// in one pass over K and V with the running maximum m and sum l of the softmax (base 2).
+// with the running maximum m and sum l of the softmax (base 2).
 //
-// What bounds it: every key and value row is read once and used by G T rows (G query heads per kv
-// head, T new tokens), 4 G T flops per 2 x 2 bytes (bf16): HBM, until G T is near 64.  So the design
-// is a stream of cache tiles with little else:
+// What bounds it: a key and value row is read once for every 16 of the G T rows that use it (G query heads per
+// kv head, T new tokens), 4 flops per row and 2 x 2 bytes (bf16).  Up to 8 rows that is HBM; from 9 on, with a cap
+// or an e4m3 cache first, the latency of dependent instructions.  So the design is a stream of cache tiles
+// with little else:
 //   - Split: the (sequence, kv head, row block) units are laid end to end as blocks of one tile of keys
 //     per warp, and every CTA (two or three per SM) takes an equal share of all blocks, wherever it
 //     begins and ends, so ragged lengths cost no balance.  A unit that several CTAs share leaves fp32
@@ -29,8 +30,8 @@
 //     below that of the bf16 output.  e4m3 cache: codes are exact in fp16; the key's scale multiplies
 //     the score, and the value's enters the exponent, w_j = 2^(z_j + log2 s_j - M) with M the row's
 //     reference of that sum (within 2 of its maximum); times 2^14 it is rounded to fp16 (2^-11 down to
-//     2^-28 of 2^M, at worst by 2^-39 of it; moving M only past 2^8, times 2^7, costs 2^7 of that and saves 1.0 us
-//     of 174.7 at 8 sequences to 131072, 0.5 of 32.5 at 48 to 8192).  The row's sum adds w_j / s_j in fp32 before that
+//     2^-28 of 2^M, at worst by 2^-39 of it; moving M only past 2^8, times 2^7, costs 2^7 of that and saves 1.5 us
+//     of 175.4 at 8 sequences to 131072, 0.4 of 32.8 at 48 to 8192).  The row's sum adds w_j / s_j in fp32 before that
 //     rounding.  q (bf16) is scaled by a power of two per row to fit fp16.
 #include <cuda_fp16.h>
 
