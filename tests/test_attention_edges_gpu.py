@@ -184,6 +184,19 @@ def test_decode_largest_queries(cuda_device):
         within(lse, l, lt, "lse")
 
 
+@pytest.mark.parametrize("softcap,window", [(0.0, 0), (30.0, 50)])
+def test_decode_scales_over_the_allowed_range(cuda_device, softcap, window):
+    """Value scales from about 2^-58 to 2^24: keys of either kind count in the sums (lse shows it)."""
+    def mutate(q, kc, vc, ks, vs, tab):
+        ok = ~torch.isnan(vs)
+        small = torch.rand(vs.shape, generator=torch.Generator().manual_seed(3)) < 0.5
+        vs[ok & small] *= 2.0 ** -51
+        vs[ok & ~small] *= 2.0 ** 31
+    out, lse, o, l, ot, lt = run_decode([500, 77, 3], 2, 2, 4, 128, 16, True, mutate=mutate, softcap=softcap, window=window)
+    within(out, o, ot, "out")
+    within(lse, l, lt, "lse")
+
+
 def test_decode_small_weights_keep_their_bits(cuda_device):
     """e4m3 cache: channels to which only keys of weights 2^-22 to 2^-27 of the largest add.  A weight is rounded to
     fp16 as p s 2^14 relative to a reference within a factor of two of the largest: 2^-11 of it down to 2^-28 of the
